@@ -87,7 +87,7 @@ def draw(rng):
         experts = rng.choice([8, 64, 128])
         topk = rng.randrange(1, 9)
         hidden = 8 * _log(rng, 16, 1024)
-        most = (8192 if op == "combine" else 4096) * 8 * 7168 // (topk * hidden)
+        most = 1_000_000_000 // (hidden * (2 * topk + 8 if op == "combine" else 4 * topk + 4))
         tokens = _log(rng, 1, min(16384, most))
         if op == "combine_bwd":
             return dict(op=op, tokens=tokens, hidden=hidden, topk=topk, experts=experts)
