@@ -56,7 +56,8 @@
  * Families: block quantize / dequantize (dense and strided); the LoRA merge
  * with weight fake-quant; block-scaled GEMMs (fp32 scales, MXFP8, NVFP4,
  * grouped MXFP8); the bf16 GEMMs of the QAT backward; the MoE FP8 dispatch;
- * status and error queries.
+ * RMS norm into 8-bit operands; the expert gate and the combination of the
+ * experts' rows; few rows times NVFP4 weights; status and error queries.
  */
 #ifndef FPQ_H
 #define FPQ_H
@@ -495,6 +496,192 @@ FPQ_API fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const
                                    const int32_t* group_offsets, int32_t groups,
                                    int64_t total_m, int64_t n, int64_t k, void* c,
                                    int32_t c_dtype, void* stream);
+
+/*
+ * fpq_rmsnorm_quantize -- RMS norm with the residual's addition and a
+ * block-scaled 8-bit output: the operand of the block-scaled products straight
+ * from the residual stream [DS "Как FP8 встроен в DeepSeek V3" (online
+ * activation quantization); "Какие операции нельзя бездумно переводить в FP8"
+ * (the norm itself stays in higher precision)].  Per row, in fp32:
+ *   s = x + residual,  rstd = 1 / sqrt(sum s^2 / cols + eps),  y = (s rstd) weight
+ *
+ *   fmt        FPQ_FP8_1x128 or FPQ_MXFP8 (read only when q is given)
+ *   x          bf16 [rows, cols] with row stride ld_x elements
+ *   residual   bf16 [rows, cols], or NULL
+ *   weight     bf16 [cols]
+ *   h          bf16(s) [rows, cols] (optional output; may be the residual's
+ *              buffer, or x's when ld_x = cols)
+ *   y          bf16(y) [rows, cols] (optional output)
+ *   q, scales  codes and scales of the fp32 y, by fmt's rules and layout
+ *              (optional outputs, both or neither)
+ *   rstd       fp32 [rows] (optional output, kept for the backward pass)
+ *
+ * At least one of y and q.  The codes are those of y before its rounding to
+ * bf16.  Other overlaps between inputs and outputs are not allowed.
+ *
+ * Requires 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768] (of 128 with
+ * FPQ_FP8_1x128 codes, of 32 with FPQ_MXFP8), ld_x >= cols a multiple of 8,
+ * eps finite and >= 0, every pointer 16-byte aligned.  rows = 0 does nothing.
+ * Errors: FPQ_ERR_INVALID_ARG, FPQ_ERR_ALIGNMENT, FPQ_ERR_UNSUPPORTED (another
+ * format), FPQ_ERR_CUDA.
+ */
+FPQ_API fpq_status fpq_rmsnorm_quantize(fpq_format fmt, const void* x, int64_t ld_x, const void* residual,
+                                        const void* weight, int64_t rows, int64_t cols, float eps, void* h, void* y,
+                                        void* q, void* scales, float* rstd, void* stream);
+
+/*
+ * fpq_rmsnorm_backward -- gradients of fpq_rmsnorm_quantize for the gradient
+ * dy of y (the quantizer passes gradients unchanged, as in fpq_qat_backward)
+ * and, where the residual stream goes on, the gradient dres of h:
+ *   dx = dres + rstd (g - xhat sum(g xhat) / cols),  g = dy weight, xhat = x rstd
+ *   dweight = sum over rows of dy xhat
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy         bf16 [rows, cols]
+ *   x          the normed rows: x (row stride ld_x elements), or h where a
+ *              residual was added
+ *   rstd       fp32 [rows] as written by the forward
+ *   dres       bf16 [rows, cols], or NULL
+ *   dx         bf16 [rows, cols] (output; may be dy's or dres's buffer)
+ *   dweight    fp32 [cols] (output, or NULL)
+ *   workspace  fpq_rmsnorm_backward_workspace_bytes(rows, cols) bytes (the
+ *              current device's SM count enters the size), caller-owned, not
+ *              read before written; not needed without dweight
+ *
+ * Partial sums of dweight are added in a fixed order: repeatable results.
+ * rows = 0 writes a zero dweight.  Requirements and errors: as the forward,
+ * plus FPQ_ERR_WORKSPACE.
+ */
+FPQ_API size_t fpq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+FPQ_API fpq_status fpq_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight,
+                                        const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
+                                        float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fpq_moe_gate -- the experts of each token and their weights from the gate's
+ * logits: what fpq_moe_route and fpq_moe_dispatch_mxfp8 take as topk_ids.
+ *   score_e  softmax(logits)_e (FPQ_MOE_SOFTMAX) or 1 / (1 + exp(-logit_e))
+ *            (FPQ_MOE_SIGMOID)
+ *   key_e    logit_e without a bias, score_e + bias_e with one
+ *   groups   n_group runs of E / n_group consecutive experts; a group ranks by
+ *            the sum of its group_top (1 or 2) largest keys (scores without a
+ *            bias); only experts of the topk_group best groups are chosen
+ *   ids      the topk largest keys in descending order
+ *   weights  scale score_e; with renormalize divided by the sum of the
+ *            chosen experts' scores (0 where that sum is 0)
+ * Keys and ranks are compared as in exact arithmetic (fp64 where fp32 cannot
+ * tell two apart); equal ones go to the lowest index.  The bias enters the
+ * choice alone.
+ *
+ *   logits   bf16 or fp32 (logits_dtype: FPQ_OUT_BF16 | FPQ_OUT_F32) [tokens, E]
+ *   bias     fp32 [E], or NULL
+ *   ids      int32 [tokens, topk], distinct per token, each in [0, E) (output)
+ *   weights  fp32 [tokens, topk] (output)
+ *
+ * A logit of -inf masks an expert: score 0, chosen after every other expert
+ * that the groups allow.  A NaN key orders below -inf; a NaN or +inf logit
+ * gives its token NaN weights under the softmax where it takes part.
+ *
+ * Requires tokens >= 0, 1 <= E <= 1024, 1 <= topk <= min(32, E), tokens * topk
+ * < 2^31, n_group in [1, 32] dividing E, topk_group in [1, n_group], topk <=
+ * topk_group E / n_group, group_top <= E / n_group when n_group > 1, every
+ * pointer 16-byte aligned.  Errors: FPQ_ERR_INVALID_ARG, FPQ_ERR_ALIGNMENT,
+ * FPQ_ERR_CUDA.
+ */
+#define FPQ_MOE_SOFTMAX 0
+#define FPQ_MOE_SIGMOID 1
+FPQ_API fpq_status fpq_moe_gate(const void* logits, int32_t logits_dtype, const float* bias, int64_t tokens,
+                                int32_t num_experts, int32_t score, int32_t n_group, int32_t topk_group,
+                                int32_t group_top, int32_t topk, int32_t renormalize, float scale, int32_t* ids,
+                                float* weights, void* stream);
+
+/*
+ * fpq_moe_gate_backward -- gradient of the logits for the gradient dweights
+ * fp32 [tokens, topk] of the weights (the choice and the bias carry none).
+ * dlogits has the logits' type and shape; every element is written.  An id
+ * out of [0, E) raises FPQ_ERR_DEVICE_BAD_INPUT and is dropped.  The other
+ * arguments as in the forward call, whose ids these are.
+ */
+FPQ_API fpq_status fpq_moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* ids,
+                                         const float* dweights, int64_t tokens, int32_t num_experts, int32_t score,
+                                         int32_t topk, int32_t renormalize, float scale, void* dlogits,
+                                         void* stream);
+
+/*
+ * fpq_moe_pair_rows -- the row that fpq_moe_dispatch_mxfp8 gives each (token,
+ * choice) pair in its destination buffer: rows int32 [tokens, topk], -1 for
+ * an expert id out of range.  topk_ids, tokens, topk, num_experts, workspace
+ * and dst_row0 as passed to the dispatch call (FPQ_MOE_DIRECT: rows of the
+ * expert's receive buffer; FPQ_MOE_PACK: rows of the send buffer).  Errors:
+ * as fpq_moe_dispatch_mxfp8.
+ */
+FPQ_API fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, int32_t topk, int32_t num_experts,
+                                     const void* workspace, size_t workspace_bytes, const int64_t* dst_row0,
+                                     int32_t* rows, void* stream);
+
+/*
+ * fpq_moe_combine -- the experts' rows back at their tokens:
+ *   out[t] = add[t] + sum_j weights[t, j] y[rows[t, j]]
+ * (j ascending, fp32 fused multiply-adds from add or zero, one rounding).
+ *
+ *   y        bf16 or fp32 [y_rows, hidden]: the experts' products
+ *   rows     DEVICE int32 [tokens, topk] (fpq_moe_pair_rows), -1 for a
+ *            dropped pair, which adds nothing; NULL: pair p = t topk + j is
+ *            row p (as fpq_moe_gemv_nvfp4 writes them).  A row outside
+ *            [-1, y_rows) raises FPQ_ERR_DEVICE_BAD_INPUT and is dropped
+ *   weights  fp32 [tokens, topk]
+ *   add      bf16 [tokens, hidden] (a shared expert's output, a residual), or
+ *            NULL
+ *   out      bf16 or fp32 [tokens, hidden]; must not overlap y or add
+ *
+ * fpq_moe_combine_backward -- for the gradient dout of out:
+ *   dy[rows[t, j]] = weights[t, j] dout[t]           (y's type and shape)
+ *   dweights[t, j] = sum over hidden of dout[t] y[rows[t, j]]   (fp32)
+ * A dropped pair has a zero dweight.  Rows of dy that no pair names are left
+ * as they were.  A row may be named by one pair only.  dy must not overlap y.
+ *
+ * Requires tokens >= 0, 1 <= topk <= 32, tokens * topk < 2^31, hidden a
+ * positive multiple of 8, 0 <= y_rows < 2^31 (>= tokens * topk without rows),
+ * every pointer 16-byte aligned.  Errors: FPQ_ERR_INVALID_ARG,
+ * FPQ_ERR_ALIGNMENT, FPQ_ERR_CUDA.
+ */
+FPQ_API fpq_status fpq_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, const int32_t* rows,
+                                   const float* weights, int64_t tokens, int32_t topk, int64_t hidden,
+                                   const void* add, void* out, int32_t out_dtype, void* stream);
+FPQ_API fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype,
+                                            int64_t y_rows, const int32_t* rows, const float* weights,
+                                            int64_t tokens, int32_t topk, int64_t hidden, void* dy, float* dweights,
+                                            void* stream);
+
+/*
+ * fpq_gemv_nvfp4, fpq_moe_gemv_nvfp4 -- products of a few bf16 rows with NVFP4
+ * weights, the form that decoding takes (the activations stay bf16):
+ *   y[m, n] = g sum_k x[m, k] e2m1(W[n, k]) e4m3(S[n, k/16])
+ * Weights are decoded exactly, sums are fp32, g multiplies the sum.
+ *
+ * Dense form:
+ *   x            bf16 [m, k], 0 <= m <= 16
+ *   wq, ws, wg   uint8 [n, k/2] packed E2M1, uint8 [n, k/16] E4M3, fp32 [1]
+ *                (as written by fpq_quantize_block with FPQ_NVFP4)
+ *   y            bf16 or fp32 [m, n]
+ * Expert form, one matrix per expert and one row per (token, choice) pair:
+ *   x            bf16 [tokens, k], or [tokens * topk, k] with x_per_pair = 1
+ *   ids          DEVICE int32 [tokens, topk]; an id out of [0, E) raises
+ *                FPQ_ERR_DEVICE_BAD_INPUT and its row of y is zero
+ *   wq, ws, wg   [E, n, k/2], [E, n, k/16], [E]
+ *   y            bf16 or fp32 [tokens * topk, n]
+ * Each chosen expert's weights are read once however many pairs chose it (up
+ * to eight at a time).  A row's result does not depend on the other rows.
+ *
+ * Requires 1 <= n <= 2^24, k a multiple of 32 in [32, 2^17], topk in [1, 32],
+ * tokens * topk <= 1024, E in [1, 1024]; wg 4-byte aligned, the other pointers
+ * 16-byte.  Errors: FPQ_ERR_INVALID_ARG, FPQ_ERR_ALIGNMENT, FPQ_ERR_CUDA.
+ */
+FPQ_API fpq_status fpq_gemv_nvfp4(const void* x, int64_t m, const void* wq, const void* ws, const float* wg,
+                                  int64_t n, int64_t k, void* y, int32_t y_dtype, void* stream);
+FPQ_API fpq_status fpq_moe_gemv_nvfp4(const void* x, int32_t x_per_pair, const int32_t* ids, int64_t tokens,
+                                      int32_t topk, int32_t num_experts, const void* wq, const void* ws,
+                                      const float* wg, int64_t n, int64_t k, void* y, int32_t y_dtype, void* stream);
 
 /*
  * fpq_quantize_nvfp4_noalloc -- NVFP4 quantization (same outputs, layouts and

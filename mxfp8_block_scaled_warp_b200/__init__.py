@@ -10,14 +10,17 @@ FPQ_ERR_UNSUPPORTED on a device that is not sm_100.
 
 The ``fpq_*`` functions mirror the C entry points one to one (tensors in
 place of pointers, the current torch stream by default).  ``quantize``,
-``dequantize``, ``lora_merge_fakequant``, ``scaled_gemm`` and
-``grouped_scaled_gemm`` are conveniences that allocate the outputs with
+``dequantize``, ``lora_merge_fakequant``, ``scaled_gemm``,
+``grouped_scaled_gemm``, ``rmsnorm_quantize``, ``rmsnorm_backward`` and
+``gemv_nvfp4`` are conveniences that allocate the outputs with
 torch and call them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -35,6 +38,10 @@ __all__ = [
     "fpq_quantize_nvfp4_noalloc", "NOALLOC_NVFP4_MAX_BATCH",
     "quantize", "dequantize", "lora_merge_fakequant", "scaled_gemm", "scaled_gemm_nvfp4", "grouped_scaled_gemm",
     "scale_shape", "code_shape", "gemm_bf16", "qat_backward",
+    "fpq_rmsnorm_quantize", "fpq_rmsnorm_backward_workspace_bytes", "fpq_rmsnorm_backward",
+    "fpq_moe_gate", "fpq_moe_gate_backward", "fpq_moe_pair_rows", "fpq_moe_combine", "fpq_moe_combine_backward",
+    "fpq_gemv_nvfp4", "fpq_moe_gemv_nvfp4", "MOE_SOFTMAX", "MOE_SIGMOID",
+    "RmsNorm", "rmsnorm_quantize", "rmsnorm_backward", "gemv_nvfp4",
 ]
 
 FP8_1x128, FP8_128x128, MXFP8, NVFP4 = 0, 1, 2, 3
@@ -99,6 +106,16 @@ def _load() -> ctypes.CDLL:
         "fpq_moe_regroup": (I32, [P, P, P, I32, I32, I32, I64, I64, P, P, P]),
         "fpq_qat_backward": (I32, [P, P, P, P, P, I64, I64, I64, I32, F, P, P, P, P, P, SZ, P]),
         "fpq_quantize_nvfp4_noalloc": (I32, [P, I64, I64, I64, P, P, P, P]),
+        "fpq_rmsnorm_quantize": (I32, [I32, P, I64, P, P, I64, I64, F, P, P, P, P, P, P]),
+        "fpq_rmsnorm_backward_workspace_bytes": (SZ, [I64, I64]),
+        "fpq_rmsnorm_backward": (I32, [P, P, I64, P, P, P, I64, I64, P, P, P, SZ, P]),
+        "fpq_moe_gate": (I32, [P, I32, P, I64, I32, I32, I32, I32, I32, I32, I32, F, P, P, P]),
+        "fpq_moe_gate_backward": (I32, [P, I32, P, P, I64, I32, I32, I32, I32, F, P, P]),
+        "fpq_moe_pair_rows": (I32, [P, I64, I32, I32, P, SZ, P, P, P]),
+        "fpq_moe_combine": (I32, [P, I32, I64, P, P, I64, I32, I64, P, P, I32, P]),
+        "fpq_moe_combine_backward": (I32, [P, I32, P, I32, I64, P, P, I64, I32, I64, P, P, P]),
+        "fpq_gemv_nvfp4": (I32, [P, I64, P, P, P, I64, I64, P, I32, P]),
+        "fpq_moe_gemv_nvfp4": (I32, [P, I32, P, I64, I32, I32, P, P, P, I64, I64, P, I32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -296,6 +313,71 @@ def fpq_quantize_nvfp4_noalloc(x, batch, rows, cols, q, scales, tensor_scale, st
 NOALLOC_NVFP4_MAX_BATCH = 4096
 
 
+def fpq_rmsnorm_quantize(fmt, x, ld_x, residual, weight, rows, cols, eps, h=None, y=None, q=None, scales=None,
+                         rstd=None, stream=None):
+    """x: a view with contiguous rows, ld_x elements apart."""
+    _check(load().fpq_rmsnorm_quantize(fmt, _ptr_rows(x), ld_x, _ptr(residual), _ptr(weight), rows, cols, float(eps),
+                                       _ptr(h), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd), _stream(stream)),
+           "fpq_rmsnorm_quantize")
+
+
+def fpq_rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return load().fpq_rmsnorm_backward_workspace_bytes(rows, cols)
+
+
+def fpq_rmsnorm_backward(dy, x, ld_x, weight, rstd, dres, rows, cols, dx, dweight=None, workspace=None, stream=None):
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().fpq_rmsnorm_backward(_ptr(dy), _ptr_rows(x), ld_x, _ptr(weight), _ptr(rstd), _ptr(dres), rows, cols,
+                                       _ptr(dx), _ptr(dweight), _ptr(workspace), wsb, _stream(stream)),
+           "fpq_rmsnorm_backward")
+
+
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+
+
+def fpq_moe_gate(logits, logits_dtype, bias, tokens, num_experts, score, n_group, topk_group, group_top, topk,
+                 renormalize, scale, ids, weights, stream=None):
+    _check(load().fpq_moe_gate(_ptr(logits), logits_dtype, _ptr(bias), tokens, num_experts, score, n_group,
+                               topk_group, group_top, topk, int(renormalize), float(scale), _ptr(ids), _ptr(weights),
+                               _stream(stream)), "fpq_moe_gate")
+
+
+def fpq_moe_gate_backward(logits, logits_dtype, ids, dweights, tokens, num_experts, score, topk, renormalize, scale,
+                          dlogits, stream=None):
+    _check(load().fpq_moe_gate_backward(_ptr(logits), logits_dtype, _ptr(ids), _ptr(dweights), tokens, num_experts,
+                                        score, topk, int(renormalize), float(scale), _ptr(dlogits),
+                                        _stream(stream)), "fpq_moe_gate_backward")
+
+
+def fpq_moe_pair_rows(topk_ids, tokens, topk, num_experts, workspace, dst_row0, rows, stream=None):
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().fpq_moe_pair_rows(_ptr(topk_ids), tokens, topk, num_experts, _ptr(workspace), wsb, _ptr(dst_row0),
+                                    _ptr(rows), _stream(stream)), "fpq_moe_pair_rows")
+
+
+def fpq_moe_combine(y, y_dtype, y_rows, rows, weights, tokens, topk, hidden, add, out, out_dtype, stream=None):
+    _check(load().fpq_moe_combine(_ptr(y), y_dtype, y_rows, _ptr(rows), _ptr(weights), tokens, topk, hidden,
+                                  _ptr(add), _ptr(out), out_dtype, _stream(stream)), "fpq_moe_combine")
+
+
+def fpq_moe_combine_backward(dout, dout_dtype, y, y_dtype, y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
+                             stream=None):
+    _check(load().fpq_moe_combine_backward(_ptr(dout), dout_dtype, _ptr(y), y_dtype, y_rows, _ptr(rows),
+                                           _ptr(weights), tokens, topk, hidden, _ptr(dy), _ptr(dweights),
+                                           _stream(stream)), "fpq_moe_combine_backward")
+
+
+def fpq_gemv_nvfp4(x, m, wq, ws, wg, n, k, y, y_dtype, stream=None):
+    _check(load().fpq_gemv_nvfp4(_ptr(x), m, _ptr(wq), _ptr(ws), _ptr(wg), n, k, _ptr(y), y_dtype, _stream(stream)),
+           "fpq_gemv_nvfp4")
+
+
+def fpq_moe_gemv_nvfp4(x, x_per_pair, ids, tokens, topk, num_experts, wq, ws, wg, n, k, y, y_dtype, stream=None):
+    _check(load().fpq_moe_gemv_nvfp4(_ptr(x), int(x_per_pair), _ptr(ids), tokens, topk, num_experts, _ptr(wq),
+                                     _ptr(ws), _ptr(wg), n, k, _ptr(y), y_dtype, _stream(stream)),
+           "fpq_moe_gemv_nvfp4")
+
+
 def fpq_get_device_error(stream=None) -> int:
     code = ctypes.c_int32(0)
     _check(load().fpq_get_device_error(_stream(stream), ctypes.byref(code)), "fpq_get_device_error")
@@ -424,3 +506,138 @@ def grouped_scaled_gemm(fmt, aq, as_, bq, bs, group_offsets, out_dtype=torch.bfl
     fpq_grouped_scaled_gemm(fmt, aq, as_, bq, bs, group_offsets, groups, total_m, n, k, c,
                             OUT_F32 if out_dtype == torch.float32 else OUT_BF16, stream)
     return c
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _launch_on(stream, *tensors):
+    """Context of a call on the given tensors (None left out), which must share
+    one CUDA device: that device is current (the library launches on the
+    current device), and so is `stream` if given, so that the outputs and
+    workspaces allocated inside belong to the stream that uses them."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("tensors must live on the same device")
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the library must live on a CUDA device")
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device != dev:
+            raise ValueError("the stream must be on the tensors' device")
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _out_type(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return OUT_BF16
+    if dtype == torch.float32:
+        return OUT_F32
+    raise ValueError("expected bfloat16 or float32")
+
+
+class RmsNorm(NamedTuple):
+    y: torch.Tensor | None       # bf16 [rows, cols]
+    q: torch.Tensor | None       # uint8 [rows, cols] E4M3 codes
+    scales: torch.Tensor | None  # fp32 [rows, cols / 128] or uint8 [rows, cols / 32]
+    h: torch.Tensor | None       # bf16 [rows, cols]: x + residual
+    rstd: torch.Tensor | None    # fp32 [rows]
+
+
+def _rows_view(x, what):
+    """(row stride) of a 2-D view with contiguous rows."""
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2, f"need {what} bf16 [rows, cols]")
+    _need(x.stride(1) == 1 or x.shape[1] == 1, f"the rows of {what} must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 1)
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, fmt: int | None = None, eps: float = 1e-6,
+                     residual: torch.Tensor | None = None, want_y: bool = False, want_rstd: bool = False,
+                     stream=None) -> RmsNorm:
+    """RMS norm of bf16 x [rows, cols] (rows may be apart: a column slice of a
+    wider matrix), after adding `residual` if given, with codes and scales of
+    the result in `fmt` (FP8_1x128 or MXFP8) and / or the result in bf16
+    (want_y; always without a fmt).  `h` is the sum x + residual, `rstd`
+    (want_rstd) what rmsnorm_backward needs.  Outputs not asked for are None."""
+    ld = _rows_view(x, "x")
+    rows, cols = x.shape
+    _need(weight.dtype == torch.bfloat16 and weight.shape == (cols,), "need weight bf16 [cols]")
+    _need(residual is None or (residual.dtype == torch.bfloat16 and residual.shape == x.shape),
+          "need residual bf16 of x's shape")
+    _need(fmt in (None, FP8_1x128, MXFP8), "need fmt None, FP8_1x128 or MXFP8")
+    _need(fmt is None or cols % (128 if fmt == FP8_1x128 else 32) == 0,
+          "cols is not a multiple of the format's block width")
+    with _launch_on(stream, x, weight, residual):
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)   # noqa: E731
+        q = s = h = y = rstd = None
+        if fmt is not None:
+            q, s = new((rows, cols), torch.uint8), new(scale_shape(fmt, x.shape), _scale_dtype(fmt))
+        if want_y or fmt is None:
+            y = new((rows, cols), torch.bfloat16)
+        if residual is not None:
+            h = new((rows, cols), torch.bfloat16)
+        if want_rstd:
+            rstd = new((rows,), torch.float32)
+        fpq_rmsnorm_quantize(fmt or 0, x, ld, residual, weight, rows, cols, eps, h, y, q, s, rstd, stream)
+    return RmsNorm(y, q, s, h, rstd)
+
+
+def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dres: torch.Tensor | None = None, stream=None):
+    """Gradients of rmsnorm_quantize for the gradient dy of its result and,
+    optionally, dres of its `h`: (dx bf16 [rows, cols], the gradient of x and
+    of the residual alike; dweight fp32 [cols]).  x is the normed input: the
+    forward's `h` where a residual was added, else its x."""
+    ld = _rows_view(x, "x")
+    rows, cols = x.shape
+    _need(dy.dtype == torch.bfloat16 and dy.shape == x.shape, "need dy bf16 of x's shape")
+    _need(weight.dtype == torch.bfloat16 and weight.shape == (cols,), "need weight bf16 [cols]")
+    _need(rstd.dtype == torch.float32 and rstd.shape == (rows,), "need rstd fp32 [rows]")
+    _need(dres is None or (dres.dtype == torch.bfloat16 and dres.shape == x.shape), "need dres bf16 of x's shape")
+    with _launch_on(stream, x, dy, weight, rstd, dres):
+        dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+        dw = torch.empty((cols,), dtype=torch.float32, device=x.device)
+        wsb = fpq_rmsnorm_backward_workspace_bytes(rows, cols)
+        ws = torch.empty((wsb,), dtype=torch.uint8, device=x.device) if wsb else None
+        fpq_rmsnorm_backward(dy, x, ld, weight, rstd, dres, rows, cols, dx, dw, ws, stream)
+    return dx, dw
+
+
+def gemv_nvfp4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, wg: torch.Tensor,
+               ids: torch.Tensor | None = None, out_dtype=torch.bfloat16, stream=None):
+    """Products of a few bf16 rows with NVFP4 weights as returned by
+    quantize(w, NVFP4); the activations stay bf16.
+
+    One matrix: x [m, k] (m <= 16), wq [n, k/2], ws [n, k/16], wg [1]; returns
+    [m, n].  Experts: ids int32 [tokens, topk], wq [E, n, k/2], ws [E, n, k/16],
+    wg [E], and x [tokens, k] (shared by a token's choices) or [tokens, topk, k];
+    returns [tokens, topk, n], tokens * topk <= 1024."""
+    c_type = _out_type(out_dtype)
+    _need(x.dtype == torch.bfloat16 and wq.dtype == torch.uint8 and ws.dtype == torch.uint8 and
+          wg.dtype == torch.float32, "need x bf16, wq and ws uint8, wg fp32")
+    _need(wq.dim() == (2 if ids is None else 3) and wq.dim() == ws.dim(),
+          "need wq [n, k/2] and ws [n, k/16], or [E, n, k/2] and [E, n, k/16] with ids")
+    n, k = wq.shape[-2], wq.shape[-1] * 2
+    _need(x.shape[-1] == k and ws.shape == (*wq.shape[:-1], k // 16) and k % 32 == 0,
+          "the shapes of x, wq and ws do not belong together (k a multiple of 32)")
+    with _launch_on(stream, x, wq, ws, wg, ids):
+        if ids is None:
+            _need(x.dim() == 2 and wg.numel() == 1, "need x [m, k] and wg of one element")
+            y = torch.empty((x.shape[0], n), dtype=out_dtype, device=x.device)
+            fpq_gemv_nvfp4(x, x.shape[0], wq, ws, wg, n, k, y, c_type, stream)
+            return y
+        _need(ids.dtype == torch.int32 and ids.dim() == 2, "need ids int32 [tokens, topk]")
+        experts, (tokens, topk) = wq.shape[0], ids.shape
+        _need(wg.shape == (experts,), "need wg [E]")
+        _need(x.shape in ((tokens, k), (tokens, topk, k)), "need x [tokens, k] or [tokens, topk, k]")
+        y = torch.empty((tokens, topk, n), dtype=out_dtype, device=x.device)
+        fpq_moe_gemv_nvfp4(x, x.dim() == 3, ids, tokens, topk, experts, wq, ws, wg, n, k, y, c_type, stream)
+    return y

@@ -2,6 +2,7 @@
 // codes, per-device state (SM count, error-word address) and dispatch to the
 // kernel launchers.  No allocation, no synchronization (except in
 // fpq_get_device_error), no CPU fallback.
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -21,6 +22,8 @@ void set_detail(const char* what, cudaError_t e) {
                   cudaGetErrorString(e));
 }
 void set_detail(const char* what) { std::snprintf(t_detail, sizeof(t_detail), "%s", what); }
+
+constexpr int64_t kNormMaxCols = 32768;
 
 constexpr int kMaxDevices = 64;
 struct DeviceState {
@@ -543,6 +546,254 @@ fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const void* a
     return from_cuda(fpq::launch_grouped_gemm_mxfp8(aq, as, bq, bs, group_offsets, groups, total_m, n, k, c,
                                                     c_dtype == FPQ_OUT_F32, d->err, d->sms, (cudaStream_t)stream),
                      "grouped gemm launch");
+}
+
+fpq_status fpq_rmsnorm_quantize(fpq_format fmt, const void* x, int64_t ld_x, const void* residual, const void* weight,
+                                int64_t rows, int64_t cols, float eps, void* h, void* y, void* q, void* scales,
+                                float* rstd, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (rows < 0 || rows > INT32_MAX || cols < 8 || cols % 8 || cols > kNormMaxCols || ld_x < cols || ld_x % 8 ||
+        ld_x > (1ll << 40) || !(eps >= 0.0f) || !(eps < INFINITY)) {
+        set_detail("need 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768], ld_x >= cols a multiple of 8, a finite "
+                   "eps >= 0");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (rows == 0) return FPQ_OK;                           // empty tensors have no address to check
+    if ((q == nullptr) != (scales == nullptr) || (!q && !y)) {
+        set_detail("need q with scales, or y, or all three");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (q && fmt != FPQ_FP8_1x128 && fmt != FPQ_MXFP8) {
+        set_detail("quantized norm outputs: FPQ_FP8_1x128 and FPQ_MXFP8");
+        return fmt == FPQ_FP8_128x128 || fmt == FPQ_NVFP4 ? FPQ_ERR_UNSUPPORTED : FPQ_ERR_INVALID_ARG;
+    }
+    if (q && cols % block_cols(fmt)) {
+        set_detail("cols is not a multiple of the format's block width");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if ((st = check_ptrs({x, weight})) != FPQ_OK) return st;
+    for (const void* p : {residual, (const void*)h, (const void*)y, (const void*)q, (const void*)scales,
+                          (const void*)rstd})
+        if (p && !aligned16(p)) { set_detail("pointer not 16-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_rmsnorm_quantize(fmt, x, ld_x, residual, weight, rows, cols, eps, h, y, q, scales,
+                                                  rstd, d->sms, (cudaStream_t)stream),
+                     "rmsnorm launch");
+}
+
+size_t fpq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 8 || cols % 8 || cols > kNormMaxCols) return 0;
+    return fpq::rmsnorm_backward_workspace_bytes(rows, cols, fpq::current_sms());
+}
+
+fpq_status fpq_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight, const float* rstd,
+                                const void* dres, int64_t rows, int64_t cols, void* dx, float* dweight,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (rows < 0 || rows > INT32_MAX || cols < 8 || cols % 8 || cols > kNormMaxCols || ld_x < cols || ld_x % 8 ||
+        ld_x > (1ll << 40)) {
+        set_detail("need 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768], ld_x >= cols a multiple of 8");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (rows > 0 && (st = check_ptrs({dy, x, weight, rstd, dx})) != FPQ_OK) return st;
+    if ((dres && !aligned16(dres)) || (dweight && !aligned16(dweight))) {
+        set_detail("pointer not 16-byte aligned");
+        return FPQ_ERR_ALIGNMENT;
+    }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    const size_t need = dweight ? fpq::rmsnorm_backward_workspace_bytes(rows, cols, d->sms) : 0;
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) {
+        set_detail("need a 16-byte aligned workspace of fpq_rmsnorm_backward_workspace_bytes() bytes");
+        return FPQ_ERR_WORKSPACE;
+    }
+    return from_cuda(fpq::launch_rmsnorm_backward(dy, x, ld_x, weight, rstd, dres, rows, cols, dx, dweight, workspace,
+                                                  d->sms, (cudaStream_t)stream),
+                     "rmsnorm backward launch");
+}
+
+fpq_status fpq_moe_gate(const void* logits, int32_t logits_dtype, const float* bias, int64_t tokens,
+                        int32_t num_experts, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                        int32_t topk, int32_t renormalize, float scale, int32_t* ids, float* weights, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (tokens < 0 || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || topk > num_experts ||
+        tokens * topk >= (1ll << 31) || (logits_dtype != FPQ_OUT_BF16 && logits_dtype != FPQ_OUT_F32) ||
+        (score != FPQ_MOE_SOFTMAX && score != FPQ_MOE_SIGMOID) || (renormalize != 0 && renormalize != 1)) {
+        set_detail("need tokens >= 0, num_experts in [1, 1024], topk in [1, min(32, num_experts)], tokens * topk < "
+                   "2^31, bf16 or fp32 logits, a known score, renormalize 0|1");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (n_group < 1 || n_group > 32 || num_experts % n_group || topk_group < 1 || topk_group > n_group ||
+        (group_top != 1 && group_top != 2) || (n_group > 1 && group_top > num_experts / n_group) ||
+        topk > topk_group * (num_experts / n_group)) {
+        set_detail("need n_group in [1, 32] dividing num_experts, topk_group in [1, n_group] with room for topk "
+                   "experts, group_top 1|2 of at least as many experts per group");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({logits, ids, weights})) != FPQ_OK) return st;
+    if (bias && !aligned16(bias)) { set_detail("bias not 16-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_moe_gate(logits, logits_dtype == FPQ_OUT_F32, bias, tokens, num_experts,
+                                          score == FPQ_MOE_SIGMOID, topk_group < n_group ? n_group : 1, topk_group,
+                                          group_top, topk, renormalize, scale, ids, weights, (cudaStream_t)stream),
+                     "moe gate launch");
+}
+
+fpq_status fpq_moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* ids, const float* dweights,
+                                 int64_t tokens, int32_t num_experts, int32_t score, int32_t topk,
+                                 int32_t renormalize, float scale, void* dlogits, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (tokens < 0 || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) ||
+        (logits_dtype != FPQ_OUT_BF16 && logits_dtype != FPQ_OUT_F32) ||
+        (score != FPQ_MOE_SOFTMAX && score != FPQ_MOE_SIGMOID) || (renormalize != 0 && renormalize != 1)) {
+        set_detail("need tokens >= 0, num_experts in [1, 1024], topk in [1, 32], tokens * topk < 2^31, bf16 or fp32 "
+                   "logits, a known score, renormalize 0|1");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({logits, ids, dweights, dlogits})) != FPQ_OK) return st;
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_moe_gate_backward(logits, logits_dtype == FPQ_OUT_F32, ids, dweights, tokens,
+                                                   num_experts, score == FPQ_MOE_SIGMOID, topk, renormalize, scale,
+                                                   dlogits, d->err, (cudaStream_t)stream),
+                     "moe gate backward launch");
+}
+
+fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, int32_t topk, int32_t num_experts,
+                             const void* workspace, size_t workspace_bytes, const int64_t* dst_row0, int32_t* rows,
+                             void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (tokens < 0 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || num_experts < 1 ||
+        num_experts > 1024) {
+        set_detail("need tokens >= 0, topk in [1, 32], tokens * topk < 2^31, num_experts in [1, 1024]");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({topk_ids, dst_row0, rows})) != FPQ_OK) return st;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < fpq::moe_route_workspace_bytes(tokens, num_experts)) {
+        set_detail("need the workspace that fpq_moe_route wrote");
+        return FPQ_ERR_WORKSPACE;
+    }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_moe_pair_rows(topk_ids, tokens, topk, num_experts, workspace, dst_row0, rows,
+                                               (cudaStream_t)stream),
+                     "moe pair rows launch");
+}
+
+namespace {
+fpq_status check_combine(int64_t y_rows, const int32_t* rows, int64_t tokens, int32_t topk, int64_t hidden,
+                         int32_t y_dtype, int32_t o_dtype) {
+    if (tokens < 0 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || hidden < 8 || hidden % 8 ||
+        hidden > (1 << 24) || y_rows < 0 || y_rows >= (1ll << 31) ||
+        (y_dtype != FPQ_OUT_BF16 && y_dtype != FPQ_OUT_F32) || (o_dtype != FPQ_OUT_BF16 && o_dtype != FPQ_OUT_F32)) {
+        set_detail("need tokens >= 0, topk in [1, 32], tokens * topk < 2^31, hidden a positive multiple of 8, "
+                   "0 <= y_rows < 2^31, bf16 or fp32 types");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (!rows && y_rows < tokens * topk) {
+        set_detail("without a row map y needs tokens * topk rows");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    return FPQ_OK;
+}
+}  // namespace
+
+fpq_status fpq_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, const int32_t* rows, const float* weights,
+                           int64_t tokens, int32_t topk, int64_t hidden, const void* add, void* out,
+                           int32_t out_dtype, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st = check_combine(y_rows, rows, tokens, topk, hidden, y_dtype, out_dtype);
+    if (st != FPQ_OK) return st;
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({weights, out})) != FPQ_OK) return st;
+    if (y_rows > 0 && (st = check_ptrs({y})) != FPQ_OK) return st;
+    if ((rows && !aligned16(rows)) || (add && !aligned16(add))) {
+        set_detail("pointer not 16-byte aligned");
+        return FPQ_ERR_ALIGNMENT;
+    }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_moe_combine(y, y_dtype == FPQ_OUT_F32, y_rows, rows, weights, tokens, topk, hidden,
+                                             add, out, out_dtype == FPQ_OUT_F32, d->err, (cudaStream_t)stream),
+                     "moe combine launch");
+}
+
+fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype,
+                                    int64_t y_rows, const int32_t* rows, const float* weights, int64_t tokens,
+                                    int32_t topk, int64_t hidden, void* dy, float* dweights, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st = check_combine(y_rows, rows, tokens, topk, hidden, y_dtype, dout_dtype);
+    if (st != FPQ_OK) return st;
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({dout, weights, dweights})) != FPQ_OK) return st;
+    if (y_rows > 0 && (st = check_ptrs({y, dy})) != FPQ_OK) return st;
+    if (rows && !aligned16(rows)) { set_detail("pointer not 16-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_moe_combine_backward(dout, dout_dtype == FPQ_OUT_F32, y, y_dtype == FPQ_OUT_F32,
+                                                      y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
+                                                      d->err, (cudaStream_t)stream),
+                     "moe combine backward launch");
+}
+
+namespace {
+fpq_status check_gemv(int64_t n, int64_t k, int32_t y_dtype, const float* wg) {
+    if (n < 1 || n > (1 << 24) || k < 32 || k % 32 || k > (1 << 17) ||
+        (y_dtype != FPQ_OUT_BF16 && y_dtype != FPQ_OUT_F32)) {
+        set_detail("need 1 <= n <= 2^24, k a multiple of 32 in [32, 2^17], a bf16 or fp32 result");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if (!wg) { set_detail("null tensor scale pointer"); return FPQ_ERR_INVALID_ARG; }
+    if (reinterpret_cast<uintptr_t>(wg) & 3) { set_detail("tensor scales must be 4-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    return FPQ_OK;
+}
+}  // namespace
+
+fpq_status fpq_gemv_nvfp4(const void* x, int64_t m, const void* wq, const void* ws, const float* wg, int64_t n,
+                          int64_t k, void* y, int32_t y_dtype, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (m < 0 || m > 16) { set_detail("need 0 <= m <= 16 (more rows: fpq_scaled_gemm_nvfp4)"); return FPQ_ERR_INVALID_ARG; }
+    if ((st = check_gemv(n, k, y_dtype, wg)) != FPQ_OK) return st;
+    if (m == 0) return FPQ_OK;
+    if ((st = check_ptrs({x, wq, ws, y})) != FPQ_OK) return st;
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_gemv_nvfp4(x, m, 1, nullptr, 1, wq, ws, wg, n, k, y, y_dtype == FPQ_OUT_F32, d->err,
+                                            d->sms, (cudaStream_t)stream),
+                     "nvfp4 gemv launch");
+}
+
+fpq_status fpq_moe_gemv_nvfp4(const void* x, int32_t x_per_pair, const int32_t* ids, int64_t tokens, int32_t topk,
+                              int32_t num_experts, const void* wq, const void* ws, const float* wg, int64_t n,
+                              int64_t k, void* y, int32_t y_dtype, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st;
+    if (tokens < 0 || topk < 1 || topk > 32 || tokens > 1024 || tokens * topk > 1024 || num_experts < 1 ||
+        num_experts > 1024 || (x_per_pair != 0 && x_per_pair != 1)) {
+        set_detail("need tokens >= 0, topk in [1, 32], tokens * topk <= 1024 (more: fpq_grouped_scaled_gemm), "
+                   "num_experts in [1, 1024], x_per_pair 0|1");
+        return FPQ_ERR_INVALID_ARG;
+    }
+    if ((st = check_gemv(n, k, y_dtype, wg)) != FPQ_OK) return st;
+    if (tokens == 0) return FPQ_OK;
+    if ((st = check_ptrs({x, ids, wq, ws, y})) != FPQ_OK) return st;
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    return from_cuda(fpq::launch_gemv_nvfp4(x, tokens * topk, x_per_pair ? 1 : topk, ids, num_experts, wq, ws, wg, n,
+                                            k, y, y_dtype == FPQ_OUT_F32, d->err, d->sms, (cudaStream_t)stream),
+                     "nvfp4 expert gemv launch");
 }
 
 fpq_status fpq_get_device_error(void* stream, int32_t* code) {

@@ -1,0 +1,265 @@
+// moe_combine.cu -- the way back of a mixture-of-experts layer: each token's
+// expert rows, weighted and added, and the backward pass; and the row of
+// every (token, choice) pair in the dispatched buffer.
+//
+//   out[t]    = add[t] + sum_j weights[t, j] y[row(t, j)]      j ascending, fp32, one rounding
+//   dy[row]   = weights[t, j] dout[t]
+//   dweights[t, j] = sum_h dout[t, h] y[row(t, j), h]          fp32
+//
+// A pair's row is rows[t, j], or its own index t topk + j without a row map;
+// -1 means the pair was dropped: it adds nothing, and its dweight is 0.
+// Rows are gathered, never scattered with atomics: every output has one
+// writer and a fixed order of additions.
+//
+// Bound by HBM: the forward reads topk rows and writes one per token, the
+// backward reads and writes topk rows.  Every thread keeps the loads of up
+// to eight rows' vectors in flight.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fpq {
+
+namespace {
+
+constexpr int kBatch = 8;                 // rows in flight per thread
+constexpr int kCombineThreads = 256;
+
+// Eight consecutive elements as fp32; index in units of eight.
+template <bool F32> struct Vec8;
+template <> struct Vec8<false> {
+    uint4 a;
+    __device__ __forceinline__ void load(const void* p, int64_t v) { a = ld_stream(static_cast<const uint4*>(p) + v); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = bf16_lo(a.x); f[1] = bf16_hi(a.x); f[2] = bf16_lo(a.y); f[3] = bf16_hi(a.y);
+        f[4] = bf16_lo(a.z); f[5] = bf16_hi(a.z); f[6] = bf16_lo(a.w); f[7] = bf16_hi(a.w);
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t v, const float (&f)[8]) {
+        st_v4(static_cast<uint4*>(p) + v, make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
+                                                     f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7])));
+    }
+};
+template <> struct Vec8<true> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* p, int64_t v) {
+        a = ld_stream(static_cast<const uint4*>(p) + 2 * v);
+        b = ld_stream(static_cast<const uint4*>(p) + 2 * v + 1);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+        f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t v, const float (&f)[8]) {
+        uint4* o = static_cast<uint4*>(p) + 2 * v;
+        st_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        st_v4(o + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+    }
+};
+
+struct CombineArgs {
+    const void* y;
+    int64_t y_rows;
+    const int32_t* rows;        // [tokens, topk], or nullptr
+    const float* weights;       // [tokens, topk]
+    int64_t tokens;
+    int topk, nvec;
+    const void* add;            // forward: bf16 [tokens, hidden], or nullptr
+    const void* dout;           // backward
+    void* out;                  // forward: [tokens, hidden]; backward: dy
+    float* dweights;
+    uint32_t* err;
+};
+
+// Row of pair p, -1 if it is dropped or outside the buffer.
+__device__ __forceinline__ int64_t pair_row(const CombineArgs& a, int64_t p, bool report) {
+    if (!a.rows) return p;
+    const int32_t r = __ldg(a.rows + p);
+    if (r >= -1 && r < a.y_rows) return r;
+    if (report) raise_device_error(a.err, FPQ_ERR_DEVICE_BAD_INPUT);
+    return -1;
+}
+
+// CTA (x, y): vectors [256 y, 256 y + 256) of token x's row.
+template <bool Y32, bool OUT32>
+__global__ void __launch_bounds__(kCombineThreads)
+moe_combine_kernel(const CombineArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t tok = blockIdx.x;
+    const int v = blockIdx.y * blockDim.x + threadIdx.x;
+    if (v >= a.nvec) return;
+    float acc[8];
+    if (a.add) {
+        Vec8<false> u;
+        u.load(a.add, tok * a.nvec + v);
+        u.get(acc);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    }
+    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
+        Vec8<Y32> u[kBatch];
+        float w[kBatch];
+        bool ok[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            ok[j] = j0 + j < a.topk;
+            if (!ok[j]) continue;
+            const int64_t p = tok * a.topk + j0 + j, r = pair_row(a, p, threadIdx.x == 0);
+            ok[j] = r >= 0;
+            if (!ok[j]) continue;
+            w[j] = __ldg(a.weights + p);
+            u[j].load(a.y, r * a.nvec + v);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (!ok[j]) continue;
+            float f[8];
+            u[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+        }
+    }
+    Vec8<OUT32>::store(a.out, tok * a.nvec + v, acc);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// One CTA per token: dout's vectors are read once per eight choices (from L1
+// after the first), each y vector once; the dots are reduced at the end.
+template <bool Y32, bool D32>
+__global__ void __launch_bounds__(kCombineThreads)
+moe_combine_bwd_kernel(const CombineArgs a) {
+    __shared__ float red[kCombineThreads / 32][kBatch];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t tok = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
+        int64_t r[kBatch];
+        float w[kBatch], dot[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t p = tok * a.topk + j0 + j;
+            r[j] = j0 + j < a.topk ? pair_row(a, p, threadIdx.x == 0) : -1;
+            w[j] = r[j] >= 0 ? __ldg(a.weights + p) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) {
+            Vec8<D32> d;
+            Vec8<Y32> u[kBatch];
+            d.load(a.dout, tok * a.nvec + v);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (r[j] >= 0) u[j].load(a.y, r[j] * a.nvec + v);
+            float df[8];
+            d.get(df);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (r[j] < 0) continue;
+                float f[8];
+                u[j].get(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[j] = fmaf(df[i], f[i], dot[j]);
+                    f[i] = w[j] * df[i];
+                }
+                Vec8<Y32>::store(a.out, r[j] * a.nvec + v, f);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float s = warp_sum(dot[j]);
+            if (lane == 0) red[warp][j] = s;
+        }
+        __syncthreads();
+        if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < a.topk) {
+            float s = 0.0f;
+            for (int i = 0; i < warps; ++i) s += red[i][threadIdx.x];
+            a.dweights[tok * a.topk + j0 + threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// rows[t, j] of every pair: dst_row0 of its expert + its slot, the slot as
+// the dispatch kernel counts it (one warp per chunk of tokens, from the
+// chunk's slot bases, in token then choice order).  -1 for an id out of range.
+constexpr int kRowWarps = 8;
+
+__global__ void __launch_bounds__(32 * kRowWarps)
+moe_pair_rows_kernel(const int32_t* __restrict__ ids, int64_t tokens, int topk, int experts,
+                     const int32_t* __restrict__ base, int64_t tpc, int64_t chunks,
+                     const int64_t* __restrict__ dst_row0, int32_t* __restrict__ rows) {
+    extern __shared__ int32_t run_all[];                    // [kRowWarps][experts] running slots
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (c >= chunks) return;
+    int32_t* run = run_all + warp * experts;
+    const int64_t p0 = c * tpc * topk, p1 = min64(tokens, (c + 1) * tpc) * topk;
+    for (int e = lane; e < experts; e += 32) run[e] = base[(int64_t)e * chunks + c];
+    __syncwarp();
+    for (int64_t p = p0; p < p1; p += 32) {
+        // 32 pairs at a time: a pair's slot is its expert's running slot plus
+        // the earlier lanes with the same expert
+        const bool in = p + lane < p1;
+        const int e = in ? ids[p + lane] : -1;
+        const bool ok = e >= 0 && e < experts;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, ok ? e : -1);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        const int slot = ok ? run[e] + before : 0;
+        __syncwarp();
+        if (ok && (same >> lane) == 1u) run[e] = slot + 1;   // the last lane of the expert
+        __syncwarp();
+        if (in) rows[p + lane] = ok ? (int32_t)(dst_row0[e] + slot) : -1;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_moe_pair_rows(const int32_t* ids, int64_t tokens, int topk, int experts, const void* workspace,
+                                 const int64_t* dst_row0, int32_t* rows, cudaStream_t st) {
+    const int64_t tpc = moe_tokens_per_chunk(tokens), chunks = moe_chunks(tokens);
+    if (chunks == 0) return cudaSuccess;
+    const int32_t* base = static_cast<const int32_t*>(workspace) + (size_t)experts * (size_t)chunks;
+    return launch_pdl(moe_pair_rows_kernel, dim3((unsigned)((chunks + kRowWarps - 1) / kRowWarps)),
+                      dim3(32 * kRowWarps), kRowWarps * experts * sizeof(int32_t), st, ids, tokens, topk, experts,
+                      base, tpc, chunks, dst_row0, rows);
+}
+
+cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const int32_t* rows, const float* weights,
+                               int64_t tokens, int topk, int64_t hidden, const void* add, void* out, int out_f32,
+                               uint32_t* err, cudaStream_t st) {
+    const int nvec = (int)(hidden / 8);
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, nvec, add, nullptr, out, nullptr, err};
+    const int threads = nvec >= kCombineThreads ? kCombineThreads : (nvec + 31) / 32 * 32;
+    const dim3 grid((unsigned)tokens, (unsigned)((nvec + threads - 1) / threads)), block((unsigned)threads);
+    if (y_f32)
+        return out_f32 ? launch_pdl(moe_combine_kernel<true, true>, grid, block, 0, st, a)
+                       : launch_pdl(moe_combine_kernel<true, false>, grid, block, 0, st, a);
+    return out_f32 ? launch_pdl(moe_combine_kernel<false, true>, grid, block, 0, st, a)
+                   : launch_pdl(moe_combine_kernel<false, false>, grid, block, 0, st, a);
+}
+
+cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
+                                        const int32_t* rows, const float* weights, int64_t tokens, int topk,
+                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, cudaStream_t st) {
+    const int nvec = (int)(hidden / 8);
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, nvec, nullptr, dout, dy, dweights, err};
+    const int threads = nvec >= kCombineThreads ? kCombineThreads : (nvec + 31) / 32 * 32;
+    const dim3 grid((unsigned)tokens), block((unsigned)threads);
+    if (y_f32)
+        return dout_f32 ? launch_pdl(moe_combine_bwd_kernel<true, true>, grid, block, 0, st, a)
+                        : launch_pdl(moe_combine_bwd_kernel<true, false>, grid, block, 0, st, a);
+    return dout_f32 ? launch_pdl(moe_combine_bwd_kernel<false, true>, grid, block, 0, st, a)
+                    : launch_pdl(moe_combine_bwd_kernel<false, false>, grid, block, 0, st, a);
+}
+
+}  // namespace fpq

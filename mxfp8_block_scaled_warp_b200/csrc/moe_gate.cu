@@ -1,0 +1,427 @@
+// moe_gate.cu -- the expert gate of a mixture-of-experts layer and its
+// backward pass: scores of the gate's logits, an optional balance bias,
+// optional group-limited choice, top-k, and the routing weights.
+//
+//   score p_e = softmax(l)_e or 1 / (1 + exp(-l_e))
+//   key     k_e = l_e without a bias (both scores grow with the logit),
+//               p_e + b_e with one
+//   groups: E / n_group consecutive experts each; a group's rank is the sum
+//           of its `group_top` largest keys (of p without a bias); experts
+//           outside the topk_group best groups are not chosen
+//   ids     the topk largest keys, in order; equal keys by lowest index
+//   weights scale p_e, divided by the sum of the chosen p with `renormalize`
+//
+// Which expert is chosen must not depend on rounding.  Without a bias the
+// keys are the inputs themselves.  With one, and for the groups, a choice is
+// made on fp32 keys whose error is below half of `slack`: if only one
+// candidate lies within `slack` of the largest key, it is the largest in
+// exact arithmetic too; otherwise (under one row in a hundred for spread
+// logits, and every exact tie) the candidates' keys are recomputed in fp64.
+//
+// A logit of -inf has score 0.  A NaN key orders below every number.  A row
+// whose chosen scores sum to 0 gets zero weights.
+//
+// One warp per token, expert e = 32 i + lane in register i: the row is read
+// once, coalesced, and every step is a warp reduction.  The traffic (a
+// logit read per expert) is a few microseconds at most; what bounds the
+// kernel is the chain of topk dependent reductions per token, hidden by the
+// other warps of the SM.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fpq {
+
+namespace {
+
+constexpr int kGateWarps = 4;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+// Order-preserving patterns: larger key, larger pattern.  Below every number
+// (-inf is 0x007FFFFF): NaN 2, outside the chosen groups 1, taken or past
+// the last expert 0.
+constexpr uint32_t kTaken = 0, kOutside = 1, kNaN = 2;
+
+__device__ __forceinline__ uint32_t pattern(float f) {
+    if (f != f) return kNaN;
+    const uint32_t b = __float_as_uint(f + 0.0f);           // -0 to +0
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value(uint32_t p) {
+    if (p <= kNaN) return -INFINITY;
+    return __uint_as_float((p & 0x80000000u) ? p ^ 0x80000000u : ~p);
+}
+
+// At least twice the error of a sum of `n` fp32 keys near `key`.  An fp32
+// score (at most 1) is within 2^-18: exp and the division within a few units
+// in the last place, the softmax's sum of up to 1024 terms (at most 37
+// additions in a row) within 2^-18.7 of its value.
+__device__ __forceinline__ float slack(float key, int n) {
+    return fabsf(key) < INFINITY ? (float)n * 0x1p-17f * (1.0f + fabsf(key)) : 0.0f;
+}
+
+template <typename T> __device__ __forceinline__ float load_logit(const T* p);
+template <> __device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
+template <> __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
+    return __uint_as_float((uint32_t)__ldg(p) << 16);
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+struct GateArgs {
+    const void* logits;
+    const float* bias;          // or nullptr
+    int64_t tokens;
+    int experts, topk, n_group, topk_group, group_top;
+    int renormalize;
+    float scale;
+    int32_t* ids;
+    float* weights;
+};
+
+// The fp64 score of a logit, for the rows that need it: mx and sum are the
+// row's softmax maximum and sum.
+template <bool SIGMOID>
+__device__ __noinline__ double score64(float l, float mx, double sum) {
+    if (SIGMOID) return 1.0 / (1.0 + exp(-(double)l));
+    return mx == -INFINITY ? 0.0 : exp((double)l - (double)mx) / sum;
+}
+
+// Best of the warp's candidates (lanes with has) in fp64, the lowest index
+// among equals; a NaN orders below every number.
+__device__ __forceinline__ int best64(double key, int index, bool has) {
+    if (!(key == key)) key = -INFINITY;
+    if (!has) index = 0x7FFFFFFF;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const double k = __shfl_xor_sync(kFull, key, o);
+        const int e = __shfl_xor_sync(kFull, index, o);
+        if (e != 0x7FFFFFFF && (index == 0x7FFFFFFF || k > key || (k == key && e < index))) { key = k; index = e; }
+    }
+    return index;
+}
+
+template <typename T, bool SIGMOID, int VPT>
+__global__ void __launch_bounds__(32 * kGateWarps)
+moe_gate_kernel(const GateArgs a) {
+    extern __shared__ float sh[];                           // per warp: keys of the row, padded per 32 (groups only)
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
+    const int64_t tok = (int64_t)blockIdx.x * kGateWarps + warp;
+    if (tok >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + tok * E;
+
+    float l[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) l[i] = 32 * i + lane < E ? load_logit<T>(row + 32 * i + lane) : -INFINITY;
+
+    // softmax maximum and sum, where the scores themselves are needed
+    const bool scores = a.bias || a.n_group > 1;
+    float mx = -INFINITY, sum = 0.0f;
+    if (!SIGMOID && (scores || !a.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) mx = fmaxf(mx, l[i]);
+        mx = warp_max(mx);
+        if (mx != -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) sum += 32 * i + lane < E ? expf(l[i] - mx) : 0.0f;
+            sum = warp_sum(sum);
+        }
+    }
+    const auto score = [&](float x) {
+        if (SIGMOID) return sigmoid(x);
+        if (mx == -INFINITY) return x == x ? 0.0f : x;
+        return __fdiv_rn(expf(x - mx), sum);
+    };
+    double sum64 = 0.0;
+    const auto need64 = [&]() {                             // warp-uniform
+        if (!SIGMOID && sum64 == 0.0 && mx != -INFINITY) {
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32) sum64 += exp((double)load_logit<T>(row + e) - (double)mx);
+            sum64 = warp_sum(sum64);
+        }
+    };
+    const auto key64 = [&](int e) {                         // of p + b, or p
+        const double p = score64<SIGMOID>(load_logit<T>(row + e), mx, sum64);
+        return a.bias ? p + (double)__ldg(a.bias + e) : p;
+    };
+
+    uint32_t key[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int e = 32 * i + lane;
+        key[i] = e >= E ? kTaken : pattern(a.bias ? score(l[i]) + __ldg(a.bias + e) : l[i]);
+    }
+
+    if (a.n_group > 1) {
+        float* s = sh + warp * (E + E / 32 + 1);            // entry e at e + e / 32: a group's scan is free of conflicts
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 32 * i + lane;
+            if (e < E) s[e + i] = a.bias ? value(key[i]) : score(l[i]);
+        }
+        __syncwarp();
+        const int size = E / a.n_group;
+        // rank of group `lane`: its largest key, or its two largest
+        float first = -INFINITY, second = -INFINITY;
+        if (lane < a.n_group)
+            for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                const float v = s[e + (e >> 5)];
+                if (v > first) { second = first; first = v; }
+                else if (v > second) second = v;
+            }
+        const float rank = a.group_top == 2 ? first + second : first;
+        uint32_t gkey = lane < a.n_group ? pattern(rank) : kTaken;
+        uint32_t open = 0;                                   // chosen groups
+        for (int g = 0; g < a.topk_group; ++g) {
+            const uint32_t m = __reduce_max_sync(kFull, gkey);
+            const float least = value(m) - slack(value(m), a.group_top);
+            const bool near = gkey != kTaken && (gkey == m || (gkey > kNaN && value(gkey) >= least));
+            uint32_t cand = __ballot_sync(kFull, near);
+            int best = __ffs(cand) - 1;
+            if (cand & (cand - 1)) {
+                need64();
+                double f = -INFINITY, n = -INFINITY;
+                if (near)
+#pragma unroll 1
+                    for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                        const double v = key64(e);
+                        if (v > f) { n = f; f = v; }
+                        else if (v > n) n = v;
+                    }
+                best = best64(a.group_top == 2 ? f + n : f, lane, near);
+            }
+            open |= 1u << best;
+            if (lane == best) gkey = kTaken;
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 32 * i + lane;
+            if (e < E && !((open >> (e / size)) & 1u)) key[i] = kOutside;
+        }
+    }
+
+    int mine = 0;                                            // lane j keeps choice j
+    for (int j = 0; j < a.topk; ++j) {
+        uint32_t top = key[0];
+#pragma unroll
+        for (int i = 1; i < VPT; ++i) top = max(top, key[i]);
+        const uint32_t m = __reduce_max_sync(kFull, top);
+        int best;
+        bool resolved = false;
+        if (a.bias && m > kNaN) {
+            const uint32_t least = pattern(value(m) - slack(value(m), 1));
+            int count = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) count += key[i] >= least;
+            if (__reduce_add_sync(kFull, (unsigned)count) > 1) {
+                need64();
+                double bk = -INFINITY;
+                int be = 0;
+                bool has = false;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (key[i] >= least) {
+                        const double k = key64(32 * i + lane);
+                        if (!has || k > bk) { bk = k; be = 32 * i + lane; has = true; }
+                    }
+                best = best64(bk, be, has);
+                resolved = true;
+            }
+        }
+        if (!resolved) {
+            uint32_t e = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = VPT - 1; i >= 0; --i)
+                if (key[i] == m) e = 32 * i + lane;
+            best = (int)__reduce_min_sync(kFull, e);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (32 * i + lane == best) key[i] = kTaken;
+        if (lane == j) mine = best;
+    }
+
+    // weights of the chosen experts, choice j in lane j
+    const bool have = lane < a.topk;
+    const float x = have ? load_logit<T>(row + mine) : -INFINITY;
+    float p;
+    if (!SIGMOID && a.renormalize) {                         // softmax over the chosen logits
+        const float cm = warp_max(x);
+        p = cm == -INFINITY && !(x != x) ? 0.0f : expf(x - cm);
+    } else {
+        p = score(x);
+    }
+    if (!have) p = 0.0f;
+    if (a.renormalize) {
+        const float total = warp_sum(p);
+        p = total == 0.0f ? 0.0f : __fdiv_rn(p, total);
+    }
+    if (have) {
+        a.ids[tok * a.topk + lane] = mine;
+        a.weights[tok * a.topk + lane] = p * a.scale;
+    }
+}
+
+// ------------------------------------------------------------------ backward
+
+struct GateBwdArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* dweights;
+    int64_t tokens;
+    int experts, topk, renormalize;
+    float scale;
+    void* dlogits;
+    uint32_t* err;
+};
+
+// With w_j = scale p_j (/ sum of the chosen p) and v_j = scale dw_j:
+//   sigmoid:              dl_j = ds_j p_j (1 - p_j), 0 where not chosen,
+//     ds_j = v_j, or with renormalize (v_j - sum_i v_i p_i / P) / P, P = sum p
+//   softmax, renormalize: dl_j = c_j (v_j - sum_i v_i c_i), 0 where not
+//     chosen, c = softmax over the chosen logits
+//   softmax:              dl_e = p_e (ds_e - sum_i v_i p_i), ds_e = v_j at id j
+// Only the last one reads every logit; the others read the chosen ones.  The
+// row is assembled in shared memory and written with 16-byte stores.
+template <typename T, bool SIGMOID>
+__global__ void __launch_bounds__(32 * kGateWarps)
+moe_gate_bwd_kernel(const GateBwdArgs a) {
+    extern __shared__ __align__(16) float sh[];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts, K = a.topk;
+    const int64_t tok = (int64_t)blockIdx.x * kGateWarps + warp;
+    if (tok >= a.tokens) return;
+    float* d = sh + warp * ((E + 3) / 4 * 4);
+    const T* row = static_cast<const T*>(a.logits) + tok * E;
+
+    int id = lane < K ? a.ids[tok * K + lane] : -1;
+    if (lane < K && (id < 0 || id >= E)) {
+        raise_device_error(a.err, FPQ_ERR_DEVICE_BAD_INPUT);
+        id = -1;                                             // its gradient is dropped
+    }
+    const bool have = id >= 0;
+    const float v = have ? a.scale * a.dweights[tok * K + lane] : 0.0f;
+    const float x = have ? load_logit<T>(row + id) : -INFINITY;
+    for (int e = lane; e < E; e += 32) d[e] = 0.0f;
+    __syncwarp();
+
+    float g = 0.0f;                                          // what choice `lane` adds at its id
+    float mx = -INFINITY, sum = 0.0f, dot = 0.0f;
+    if (SIGMOID) {
+        const float p = have ? sigmoid(x) : 0.0f, q = have ? sigmoid(-x) : 0.0f;   // q = 1 - p without cancellation
+        g = v;
+        if (a.renormalize) {
+            const float P = warp_sum(p);
+            const float mean = P == 0.0f ? 0.0f : __fdiv_rn(warp_sum(v * p), P);
+            g = P == 0.0f ? 0.0f : __fdiv_rn(v - mean, P);
+        }
+        g = g * p * q;
+    } else if (a.renormalize) {
+        mx = warp_max(x);
+        const float c = have && mx != -INFINITY ? expf(x - mx) : 0.0f;
+        const float total = warp_sum(c), vc = warp_sum(v * c);
+        g = total == 0.0f ? 0.0f : __fdiv_rn(c, total) * (v - __fdiv_rn(vc, total));
+    } else {
+        for (int e = lane; e < E; e += 32) mx = fmaxf(mx, load_logit<T>(row + e));
+        mx = warp_max(mx);
+        if (mx != -INFINITY) {
+            for (int e = lane; e < E; e += 32) sum += expf(load_logit<T>(row + e) - mx);
+            sum = warp_sum(sum);
+        }
+        const float p = have && mx != -INFINITY ? __fdiv_rn(expf(x - mx), sum) : 0.0f;
+        dot = warp_sum(v * p);
+        g = v;
+    }
+    // one choice after the other, by the lane that owns the expert: an id
+    // named twice gets the sum, in the order of the choices
+    for (int j = 0; j < K; ++j) {
+        const int e = __shfl_sync(kFull, id, j);
+        const float gj = __shfl_sync(kFull, g, j);
+        if (e >= 0 && (e & 31) == lane) d[e] += gj;
+    }
+    __syncwarp();
+    if (!SIGMOID && !a.renormalize)
+        for (int e = lane; e < E; e += 32) {
+            const float p = mx != -INFINITY ? __fdiv_rn(expf(load_logit<T>(row + e) - mx), sum) : 0.0f;
+            d[e] = p * (d[e] - dot);
+        }
+    __syncwarp();
+
+    T* out = static_cast<T*>(a.dlogits) + tok * E;
+    if (sizeof(T) == 4) {
+        if (E % 4 == 0) {
+            for (int i = lane; i < E / 4; i += 32)
+                st_v4(reinterpret_cast<uint4*>(out) + i, reinterpret_cast<const uint4*>(d)[i]);
+        } else {
+            for (int e = lane; e < E; e += 32) reinterpret_cast<float*>(out)[e] = d[e];
+        }
+    } else if (E % 8 == 0) {
+        for (int i = lane; i < E / 8; i += 32) {
+            const float4 u = reinterpret_cast<const float4*>(d)[2 * i], w = reinterpret_cast<const float4*>(d)[2 * i + 1];
+            st_v4(reinterpret_cast<uint4*>(out) + i,
+                  make_uint4(f32x2_to_bf16x2(u.x, u.y), f32x2_to_bf16x2(u.z, u.w), f32x2_to_bf16x2(w.x, w.y),
+                             f32x2_to_bf16x2(w.z, w.w)));
+        }
+    } else {
+        for (int e = lane; e < E; e += 32) reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(d[e]);
+    }
+}
+
+template <typename T, bool SIGMOID>
+cudaError_t gate(const GateArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.tokens + kGateWarps - 1) / kGateWarps)), block(32 * kGateWarps);
+    const size_t smem = a.n_group > 1 ? (size_t)kGateWarps * (a.experts + a.experts / 32 + 1) * sizeof(float) : 0;
+    const int E = a.experts;
+    if (E <= 32) return launch_pdl(moe_gate_kernel<T, SIGMOID, 1>, grid, block, smem, st, a);
+    if (E <= 64) return launch_pdl(moe_gate_kernel<T, SIGMOID, 2>, grid, block, smem, st, a);
+    if (E <= 128) return launch_pdl(moe_gate_kernel<T, SIGMOID, 4>, grid, block, smem, st, a);
+    if (E <= 256) return launch_pdl(moe_gate_kernel<T, SIGMOID, 8>, grid, block, smem, st, a);
+    if (E <= 512) return launch_pdl(moe_gate_kernel<T, SIGMOID, 16>, grid, block, smem, st, a);
+    return launch_pdl(moe_gate_kernel<T, SIGMOID, 32>, grid, block, smem, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gate(const void* logits, int f32, const float* bias, int64_t tokens, int experts, int sigmoid,
+                            int n_group, int topk_group, int group_top, int topk, int renormalize, float scale,
+                            int32_t* ids, float* weights, cudaStream_t st) {
+    const GateArgs a{logits, bias, tokens, experts, topk, n_group, topk_group, group_top, renormalize, scale, ids,
+                     weights};
+    if (f32) return sigmoid ? gate<float, true>(a, st) : gate<float, false>(a, st);
+    return sigmoid ? gate<uint16_t, true>(a, st) : gate<uint16_t, false>(a, st);
+}
+
+cudaError_t launch_moe_gate_backward(const void* logits, int f32, const int32_t* ids, const float* dweights,
+                                     int64_t tokens, int experts, int sigmoid, int topk, int renormalize,
+                                     float scale, void* dlogits, uint32_t* err, cudaStream_t st) {
+    const GateBwdArgs a{logits, ids, dweights, tokens, experts, topk, renormalize, scale, dlogits, err};
+    const dim3 grid((unsigned)((tokens + kGateWarps - 1) / kGateWarps)), block(32 * kGateWarps);
+    const size_t smem = (size_t)kGateWarps * ((experts + 3) / 4 * 4) * sizeof(float);
+    if (f32)
+        return sigmoid ? launch_pdl(moe_gate_bwd_kernel<float, true>, grid, block, smem, st, a)
+                       : launch_pdl(moe_gate_bwd_kernel<float, false>, grid, block, smem, st, a);
+    return sigmoid ? launch_pdl(moe_gate_bwd_kernel<uint16_t, true>, grid, block, smem, st, a)
+                   : launch_pdl(moe_gate_bwd_kernel<uint16_t, false>, grid, block, smem, st, a);
+}
+
+}  // namespace fpq

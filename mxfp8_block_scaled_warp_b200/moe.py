@@ -18,6 +18,12 @@ run to its rank (NCCL over NVLink; no TMA of any kind touches a peer's
 memory), and a kernel regroups the rows that arrived source-major into the
 expert-then-source order.  Every step of the computation runs in the
 library's kernels; this module allocates buffers and issues the collectives.
+
+``gate`` makes the expert ids and weights from the gate's logits; ``combine``
+brings the experts' rows back to their tokens (with the row map that
+``dispatch`` fills in).  Both have backward passes.  The combination is local
+to a rank: with several ranks the experts' rows first return to the order of
+the rank's own send buffer.
 """
 from __future__ import annotations
 
@@ -26,10 +32,15 @@ from typing import NamedTuple
 import torch
 import torch.distributed as dist
 
-from . import (MOE_DIRECT, MOE_PACK, fpq_moe_dispatch_layout, fpq_moe_dispatch_mxfp8, fpq_moe_regroup,
-               fpq_moe_route, fpq_moe_route_workspace_bytes)
+from . import (MOE_DIRECT, MOE_PACK, MOE_SIGMOID, MOE_SOFTMAX, _launch_on, _need, _out_type, fpq_moe_combine,
+               fpq_moe_combine_backward, fpq_moe_dispatch_layout, fpq_moe_dispatch_mxfp8, fpq_moe_gate,
+               fpq_moe_gate_backward, fpq_moe_pair_rows, fpq_moe_regroup, fpq_moe_route,
+               fpq_moe_route_workspace_bytes)
 
-__all__ = ["Dispatched", "route", "dispatch", "split_sizes", "exchange_rows"]
+__all__ = ["Dispatched", "route", "dispatch", "split_sizes", "exchange_rows", "SOFTMAX", "SIGMOID", "gate",
+           "gate_backward", "combine", "combine_backward"]
+
+SOFTMAX, SIGMOID = MOE_SOFTMAX, MOE_SIGMOID
 
 
 class Dispatched(NamedTuple):
@@ -79,10 +90,17 @@ def _dispatch_into(x, topk_ids, num_experts, ws, dst_row0, buffers, stream=None)
                            codes_p, scales_p, cap, stream)
 
 
-def dispatch(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, group=None, stream=None) -> Dispatched:
+def dispatch(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, group=None, stream=None,
+             rows: torch.Tensor | None = None) -> Dispatched:
     """x bf16 [tokens, hidden] (hidden a multiple of 32) and topk_ids int32
     [tokens, k] on this rank's GPU; returns this rank's expert-grouped MXFP8
-    rows.  With a process group of several ranks the call is collective."""
+    rows.  With a process group of several ranks the call is collective.
+    `rows` (int32 [tokens, k], filled in) receives each pair's row: of the
+    returned buffer on one rank, of the rank's own expert-major send buffer
+    on several."""
+    pair_rows = rows
+    if pair_rows is not None and (pair_rows.dtype != torch.int32 or pair_rows.shape != topk_ids.shape):
+        raise ValueError("need rows int32 of topk_ids' shape")
     if x.dtype != torch.bfloat16 or x.dim() != 2 or topk_ids.dtype != torch.int32 or topk_ids.dim() != 2:
         raise ValueError("need x bf16 [tokens, hidden] and topk_ids int32 [tokens, k]")
     tokens, hidden = x.shape
@@ -102,6 +120,8 @@ def dispatch(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, group=No
         rows = tokens * topk_ids.shape[1]
         codes, scales = torch.empty((rows, hidden), **u8), torch.empty((rows, hidden // 32), **u8)
         _dispatch_into(x, topk_ids, num_experts, ws, dst_row0, [(codes, scales)], stream)
+        if pair_rows is not None:
+            fpq_moe_pair_rows(topk_ids, tokens, topk_ids.shape[1], num_experts, ws, dst_row0, pair_rows, stream)
         return Dispatched(codes, scales, offsets, counts_all)
     counts_flat = torch.empty((world * num_experts,), dtype=torch.int32, device=dev)
     dist.all_gather_into_tensor(counts_flat, counts, group=group)     # flat output: every backend takes it
@@ -110,6 +130,8 @@ def dispatch(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, group=No
     rows = tokens * topk_ids.shape[1]
     send_q, send_s = torch.empty((rows, hidden), **u8), torch.empty((rows, hidden // 32), **u8)
     _dispatch_into(x, topk_ids, num_experts, ws, dst_row0, [(send_q, send_s)], stream)
+    if pair_rows is not None:
+        fpq_moe_pair_rows(topk_ids, tokens, topk_ids.shape[1], num_experts, ws, dst_row0, pair_rows, stream)
     counts_host = counts_all.cpu()           # row counts of the all-to-all (waits for the counts)
     codes, scales = exchange_rows(send_q, send_s, counts_host, rank, world, num_experts, group,
                                   counts_dev=counts_all, stream=stream)
@@ -152,3 +174,91 @@ def exchange_rows(send_codes, send_scales, counts_all, rank: int, world: int, nu
     (regroup or fpq_moe_regroup)(recv_q, recv_s, counts_dev, world, num_experts, rank, hidden, rows, codes, scales,
                                  stream)
     return codes, scales
+
+
+def gate(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = None, score: int = SOFTMAX, n_group: int = 1,
+         topk_group: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """The topk experts of each token and their weights from the gate's logits
+    (bf16 or fp32 [tokens, E]): (ids int32 [tokens, topk], weights fp32).
+
+    Scores are the SOFTMAX over the experts or SIGMOID; with `bias` (fp32
+    [E], balances the load) experts are chosen by score + bias but weighted
+    by the score.  With n_group > 1 only experts of the topk_group groups
+    with the largest sums of their `group_top` best are chosen.  `renormalize`
+    makes a token's weights sum to `scale`.  Equal keys go to the lowest
+    index, and ties are judged exactly (fpq_moe_gate in include/fpq.h)."""
+    _need(logits.dim() == 2, "need logits [tokens, E]")
+    kind = _out_type(logits.dtype)
+    tokens, experts = logits.shape
+    _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (experts,)), "need bias fp32 [E]")
+    with _launch_on(stream, logits, bias):
+        ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+        fpq_moe_gate(logits, kind, bias, tokens, experts, score, n_group, topk_group, group_top, topk, renormalize,
+                     scale, ids, weights, stream)
+    return ids, weights
+
+
+def gate_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: int = SOFTMAX,
+                  renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Gradient of the logits (their type and shape) for the gradient dweights
+    fp32 [tokens, topk] of gate's weights, with the ids that gate chose."""
+    _need(logits.dim() == 2, "need logits [tokens, E]")
+    kind = _out_type(logits.dtype)
+    tokens, experts = logits.shape
+    _need(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == tokens, "need ids int32 [tokens, topk]")
+    _need(dweights.dtype == torch.float32 and dweights.shape == ids.shape, "need dweights fp32 of ids' shape")
+    with _launch_on(stream, logits, ids, dweights):
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+        fpq_moe_gate_backward(logits, kind, ids, dweights, tokens, experts, score, ids.shape[1], renormalize, scale,
+                              dlogits, stream)
+    return dlogits
+
+
+def _pairs(y, weights, rows):
+    """(rows of y, hidden) after the checks that combine and its backward share."""
+    _need(weights.dtype == torch.float32 and weights.dim() == 2, "need weights fp32 [tokens, topk]")
+    _need(y.dim() == 2 or (y.dim() == 3 and rows is None and y.shape[:2] == weights.shape),
+          "need y [rows, hidden], or [tokens, topk, hidden] without a row map")
+    _need(rows is None or (rows.dtype == torch.int32 and rows.shape == weights.shape),
+          "need rows int32 of weights' shape")
+    return y.shape[:-1].numel(), y.shape[-1]
+
+
+def combine(y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = None,
+            add: torch.Tensor | None = None, out_dtype=torch.bfloat16, stream=None):
+    """out[t] = add[t] + sum_j weights[t, j] y[rows[t, j]]: the experts' rows y
+    (bf16 or fp32 [R, hidden]) weighted and added at their tokens.  `rows` is
+    the map that dispatch fills in (-1: a dropped pair); without it y is
+    [tokens, topk, hidden] (or the same rows in two dimensions).  `add`: bf16
+    [tokens, hidden], a shared expert's output for instance."""
+    y_rows, hidden = _pairs(y, weights, rows)
+    tokens, topk = weights.shape
+    _need(add is None or (add.dtype == torch.bfloat16 and add.shape == (tokens, hidden)),
+          "need add bf16 [tokens, hidden]")
+    kind, out_kind = _out_type(y.dtype), _out_type(out_dtype)
+    with _launch_on(stream, y, weights, rows, add):
+        out = torch.empty((tokens, hidden), dtype=out_dtype, device=y.device)
+        fpq_moe_combine(y, kind, y_rows, rows, weights, tokens, topk, hidden, add, out, out_kind, stream)
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = None,
+                     dy: torch.Tensor | None = None, stream=None):
+    """Gradients of combine for the gradient dout (bf16 or fp32 [tokens,
+    hidden]) of its result: (dy of y's type and shape, dweights fp32 [tokens,
+    topk]); add's gradient is dout itself.  Rows of dy that no pair names are
+    left as they were in the buffer (`dy`, or a new one).  A row may be named
+    by one pair only."""
+    y_rows, hidden = _pairs(y, weights, rows)
+    tokens, topk = weights.shape
+    _need(dout.shape == (tokens, hidden), "need dout [tokens, hidden]")
+    _need(dy is None or (dy.dtype == y.dtype and dy.shape == y.shape), "need dy of y's type and shape")
+    kind, d_kind = _out_type(y.dtype), _out_type(dout.dtype)
+    with _launch_on(stream, y, dout, weights, rows, dy):
+        if dy is None:
+            dy = torch.empty_like(y)
+        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+        fpq_moe_combine_backward(dout, d_kind, y, kind, y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
+                                 stream)
+    return dy, dweights
