@@ -32,10 +32,9 @@ from typing import NamedTuple
 import torch
 import torch.distributed as dist
 
-from . import (MOE_DIRECT, MOE_PACK, MOE_SIGMOID, MOE_SOFTMAX, _launch_on, _need, _out_type, fpq_moe_combine,
-               fpq_moe_combine_backward, fpq_moe_dispatch_layout, fpq_moe_dispatch_mxfp8, fpq_moe_gate,
-               fpq_moe_gate_backward, fpq_moe_pair_rows, fpq_moe_regroup, fpq_moe_route,
-               fpq_moe_route_workspace_bytes)
+from . import (MOE_DIRECT, MOE_PACK, MOE_SIGMOID, MOE_SOFTMAX, _addr, _check, _contiguous, _elsewhere, _need,
+               _out_type, _stream, fpq_moe_dispatch_layout, fpq_moe_dispatch_mxfp8, fpq_moe_pair_rows,
+               fpq_moe_regroup, fpq_moe_route, fpq_moe_route_workspace_bytes, load)
 
 __all__ = ["Dispatched", "route", "dispatch", "split_sizes", "exchange_rows", "SOFTMAX", "SIGMOID", "gate",
            "gate_backward", "combine", "combine_backward"]
@@ -190,12 +189,17 @@ def gate(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = None, scor
     _need(logits.dim() == 2, "need logits [tokens, E]")
     kind = _out_type(logits.dtype)
     tokens, experts = logits.shape
-    _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (experts,)), "need bias fp32 [E]")
-    with _launch_on(stream, logits, bias):
-        ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
-        fpq_moe_gate(logits, kind, bias, tokens, experts, score, n_group, topk_group, group_top, topk, renormalize,
-                     scale, ids, weights, stream)
+    _need(bias is None or (bias.dtype is torch.float32 and bias.shape == (experts,)), "need bias fp32 [E]")
+    _contiguous(logits, bias)
+    where = _elsewhere(stream, logits, bias)
+    if where is not None:
+        with where:
+            return gate(logits, topk, bias, score, n_group, topk_group, group_top, renormalize, scale)
+    ids = logits.new_empty((tokens, topk), dtype=torch.int32)
+    weights = logits.new_empty((tokens, topk), dtype=torch.float32)
+    _check(load().fpq_moe_gate(logits.data_ptr(), kind, _addr(bias), tokens, experts, score, n_group, topk_group,
+                               group_top, topk, renormalize, scale, ids.data_ptr(), weights.data_ptr(),
+                               _stream(None)), "fpq_moe_gate")
     return ids, weights
 
 
@@ -206,18 +210,23 @@ def gate_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tenso
     _need(logits.dim() == 2, "need logits [tokens, E]")
     kind = _out_type(logits.dtype)
     tokens, experts = logits.shape
-    _need(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == tokens, "need ids int32 [tokens, topk]")
-    _need(dweights.dtype == torch.float32 and dweights.shape == ids.shape, "need dweights fp32 of ids' shape")
-    with _launch_on(stream, logits, ids, dweights):
-        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-        fpq_moe_gate_backward(logits, kind, ids, dweights, tokens, experts, score, ids.shape[1], renormalize, scale,
-                              dlogits, stream)
+    _need(ids.dtype is torch.int32 and ids.dim() == 2 and ids.shape[0] == tokens, "need ids int32 [tokens, topk]")
+    _need(dweights.dtype is torch.float32 and dweights.shape == ids.shape, "need dweights fp32 of ids' shape")
+    _contiguous(logits, ids, dweights)
+    where = _elsewhere(stream, logits, ids, dweights)
+    if where is not None:
+        with where:
+            return gate_backward(dweights, logits, ids, score, renormalize, scale)
+    dlogits = torch.empty_like(logits)
+    _check(load().fpq_moe_gate_backward(logits.data_ptr(), kind, ids.data_ptr(), dweights.data_ptr(), tokens, experts,
+                                        score, ids.shape[1], renormalize, scale, dlogits.data_ptr(), _stream(None)),
+           "fpq_moe_gate_backward")
     return dlogits
 
 
 def _pairs(y, weights, rows):
     """(rows of y, hidden) after the checks that combine and its backward share."""
-    _need(weights.dtype == torch.float32 and weights.dim() == 2, "need weights fp32 [tokens, topk]")
+    _need(weights.dtype is torch.float32 and weights.dim() == 2, "need weights fp32 [tokens, topk]")
     _need(y.dim() == 2 or (y.dim() == 3 and rows is None and y.shape[:2] == weights.shape),
           "need y [rows, hidden], or [tokens, topk, hidden] without a row map")
     _need(rows is None or (rows.dtype == torch.int32 and rows.shape == weights.shape),
@@ -237,9 +246,14 @@ def combine(y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = 
     _need(add is None or (add.dtype == torch.bfloat16 and add.shape == (tokens, hidden)),
           "need add bf16 [tokens, hidden]")
     kind, out_kind = _out_type(y.dtype), _out_type(out_dtype)
-    with _launch_on(stream, y, weights, rows, add):
-        out = torch.empty((tokens, hidden), dtype=out_dtype, device=y.device)
-        fpq_moe_combine(y, kind, y_rows, rows, weights, tokens, topk, hidden, add, out, out_kind, stream)
+    _contiguous(y, weights, rows, add)
+    where = _elsewhere(stream, y, weights, rows, add)
+    if where is not None:
+        with where:
+            return combine(y, weights, rows, add, out_dtype)
+    out = y.new_empty((tokens, hidden), dtype=out_dtype)
+    _check(load().fpq_moe_combine(y.data_ptr(), kind, y_rows, _addr(rows), weights.data_ptr(), tokens, topk, hidden,
+                                  _addr(add), out.data_ptr(), out_kind, _stream(None)), "fpq_moe_combine")
     return out
 
 
@@ -255,10 +269,15 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor,
     _need(dout.shape == (tokens, hidden), "need dout [tokens, hidden]")
     _need(dy is None or (dy.dtype == y.dtype and dy.shape == y.shape), "need dy of y's type and shape")
     kind, d_kind = _out_type(y.dtype), _out_type(dout.dtype)
-    with _launch_on(stream, y, dout, weights, rows, dy):
-        if dy is None:
-            dy = torch.empty_like(y)
-        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
-        fpq_moe_combine_backward(dout, d_kind, y, kind, y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
-                                 stream)
+    _contiguous(dout, y, weights, rows, dy)
+    where = _elsewhere(stream, y, dout, weights, rows, dy)
+    if where is not None:
+        with where:
+            return combine_backward(dout, y, weights, rows, dy)
+    if dy is None:
+        dy = torch.empty_like(y)
+    dweights = torch.empty_like(weights)
+    _check(load().fpq_moe_combine_backward(dout.data_ptr(), d_kind, y.data_ptr(), kind, y_rows, _addr(rows),
+                                           weights.data_ptr(), tokens, topk, hidden, dy.data_ptr(),
+                                           dweights.data_ptr(), _stream(None)), "fpq_moe_combine_backward")
     return dy, dweights
