@@ -8,6 +8,10 @@ when ``libfpq.so`` is missing (build it with ``python -m
 mxfp8_block_scaled_warp_b200.build``), and every call fails with
 FPQ_ERR_UNSUPPORTED on a device that is not sm_100.
 
+``rmsnorm_quantize``, ``rmsnorm_backward`` and ``gemv_nvfp4`` (and the gate
+and the combination in ``moe``) go through ``_fpq_torch.so``, which does the
+same checks and marshalling in C++: their kernels take microseconds.
+
 The ``fpq_*`` functions mirror the C entry points one to one (tensors in
 place of pointers, the current torch stream by default).  ``quantize``,
 ``dequantize``, ``lora_merge_fakequant``, ``scaled_gemm``,
@@ -18,6 +22,7 @@ torch and call them.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import NamedTuple
 
@@ -509,48 +514,33 @@ def grouped_scaled_gemm(fmt, aq, as_, bq, bs, group_offsets, out_dtype=torch.bfl
     return c
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+_ops_module = None
 
 
-def _elsewhere(stream, x, *others):
-    """None if a call on these tensors (None left out) can be issued as it is:
-    `stream` not given and their common device current.  Otherwise the context
-    to issue it in: that device is current there (the library launches on the
-    current device), and `stream` if given, so that the outputs and
-    workspaces allocated inside belong to the stream that uses them."""
-    dev = x.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must live on the same device")
-    if dev < 0:
-        raise ValueError("tensors passed to the library must live on a CUDA device")
-    if stream is None:
-        return None if dev == _device_index() else torch.cuda.device(dev)
+def _ops():
+    """The C++ module (once); ImportError if it has not been built."""
+    global _ops_module
+    if _ops_module is None:
+        load()
+        path = os.path.join(_HERE, "_fpq_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built; run `python -m mxfp8_block_scaled_warp_b200.build`")
+        spec = importlib.util.spec_from_file_location("_fpq_torch", path)
+        _ops_module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_ops_module)
+    return _ops_module
+
+
+def _on_stream(stream, x: torch.Tensor):
+    """Context in which `stream` (a torch stream or its address) is current, so
+    that the outputs and workspaces allocated inside belong to it."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.device.index != dev:
+        if not x.is_cuda:
+            raise ValueError("tensors passed to the library must live on a CUDA device")
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    if stream.device != x.device:
         raise ValueError("the stream must be on the tensors' device")
     return torch.cuda.stream(stream)
-
-
-def _contiguous(*tensors) -> None:
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors passed to the library must be contiguous")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _out_type(dtype) -> int:
-    if dtype is torch.bfloat16:
-        return OUT_BF16
-    if dtype is torch.float32:
-        return OUT_F32
-    raise ValueError("expected bfloat16 or float32")
 
 
 class RmsNorm(NamedTuple):
@@ -561,13 +551,6 @@ class RmsNorm(NamedTuple):
     rstd: torch.Tensor | None    # fp32 [rows]
 
 
-def _rows_view(x):
-    """Row stride of a 2-D view with contiguous rows."""
-    _need(x.dtype is torch.bfloat16 and x.dim() == 2, "need x bf16 [rows, cols]")
-    _need(x.stride(1) == 1 or x.shape[1] == 1, "the rows of x must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
-
-
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, fmt: int | None = None, eps: float = 1e-6,
                      residual: torch.Tensor | None = None, want_y: bool = False, want_rstd: bool = False,
                      stream=None) -> RmsNorm:
@@ -576,33 +559,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, fmt: int | None = No
     the result in `fmt` (FP8_1x128 or MXFP8) and / or the result in bf16
     (want_y; always without a fmt).  `h` is the sum x + residual, `rstd`
     (want_rstd) what rmsnorm_backward needs.  Outputs not asked for are None."""
-    ld = _rows_view(x)
-    rows, cols = x.shape
-    _need(weight.dtype is torch.bfloat16 and weight.shape == (cols,), "need weight bf16 [cols]")
-    _need(residual is None or (residual.dtype is torch.bfloat16 and residual.shape == x.shape),
-          "need residual bf16 of x's shape")
-    _need(fmt in (None, FP8_1x128, MXFP8), "need fmt None, FP8_1x128 or MXFP8")
-    _need(fmt is None or cols % (128 if fmt == FP8_1x128 else 32) == 0,
-          "cols is not a multiple of the format's block width")
-    _contiguous(weight, residual)
-    where = _elsewhere(stream, x, weight, residual)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, x):
             return rmsnorm_quantize(x, weight, fmt, eps, residual, want_y, want_rstd)
-    q = s = h = y = rstd = None
-    if fmt is not None:
-        q, s = x.new_empty((rows, cols), dtype=torch.uint8), x.new_empty(scale_shape(fmt, x.shape),
-                                                                         dtype=_scale_dtype(fmt))
-    if want_y or fmt is None:
-        y = x.new_empty((rows, cols))
-    if residual is not None:
-        h = torch.empty_like(residual)
-    if want_rstd:
-        rstd = x.new_empty((rows,), dtype=torch.float32)
-    _check(load().fpq_rmsnorm_quantize(fmt or 0, x.data_ptr(), ld, _addr(residual), weight.data_ptr(), rows, cols, eps,
-                                       _addr(h), _addr(y), _addr(q), _addr(s), _addr(rstd), _stream(None)),
-           "fpq_rmsnorm_quantize")
-    return RmsNorm(y, q, s, h, rstd)
+    return RmsNorm._make(_ops().rmsnorm_quantize(x, weight, fmt, eps, residual, want_y, want_rstd))
 
 
 def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -611,25 +571,10 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
     optionally, dres of its `h`: (dx bf16 [rows, cols], the gradient of x and
     of the residual alike; dweight fp32 [cols]).  x is the normed input: the
     forward's `h` where a residual was added, else its x."""
-    ld = _rows_view(x)
-    rows, cols = x.shape
-    _need(dy.dtype is torch.bfloat16 and dy.shape == x.shape, "need dy bf16 of x's shape")
-    _need(weight.dtype is torch.bfloat16 and weight.shape == (cols,), "need weight bf16 [cols]")
-    _need(rstd.dtype is torch.float32 and rstd.shape == (rows,), "need rstd fp32 [rows]")
-    _need(dres is None or (dres.dtype is torch.bfloat16 and dres.shape == x.shape), "need dres bf16 of x's shape")
-    _contiguous(dy, weight, rstd, dres)
-    where = _elsewhere(stream, x, dy, weight, rstd, dres)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, x):
             return rmsnorm_backward(dy, x, weight, rstd, dres)
-    dx = torch.empty_like(dy)
-    dw = x.new_empty((cols,), dtype=torch.float32)
-    wsb = fpq_rmsnorm_backward_workspace_bytes(rows, cols)
-    ws = x.new_empty((wsb,), dtype=torch.uint8) if wsb else None
-    _check(load().fpq_rmsnorm_backward(dy.data_ptr(), x.data_ptr(), ld, weight.data_ptr(), rstd.data_ptr(),
-                                       _addr(dres), rows, cols, dx.data_ptr(), dw.data_ptr(), _addr(ws), wsb,
-                                       _stream(None)), "fpq_rmsnorm_backward")
-    return dx, dw
+    return _ops().rmsnorm_backward(dy, x, weight, rstd, dres)
 
 
 def gemv_nvfp4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, wg: torch.Tensor,
@@ -641,31 +586,7 @@ def gemv_nvfp4(x: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, wg: torch.Te
     [m, n].  Experts: ids int32 [tokens, topk], wq [E, n, k/2], ws [E, n, k/16],
     wg [E], and x [tokens, k] (shared by a token's choices) or [tokens, topk, k];
     returns [tokens, topk, n], tokens * topk <= 1024."""
-    c_type = _out_type(out_dtype)
-    _need(x.dtype is torch.bfloat16 and wq.dtype is torch.uint8 and ws.dtype is torch.uint8 and
-          wg.dtype is torch.float32, "need x bf16, wq and ws uint8, wg fp32")
-    _need(wq.dim() == (2 if ids is None else 3) and wq.dim() == ws.dim(),
-          "need wq [n, k/2] and ws [n, k/16], or [E, n, k/2] and [E, n, k/16] with ids")
-    n, k = wq.shape[-2], wq.shape[-1] * 2
-    _need(k % 32 == 0 and x.shape[-1] == k and ws.shape[:-1] == wq.shape[:-1] and ws.shape[-1] == k // 16,
-          "the shapes of x, wq and ws do not belong together (k a multiple of 32)")
-    _contiguous(x, wq, ws, wg, ids)
-    where = _elsewhere(stream, x, wq, ws, wg, ids)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, x):
             return gemv_nvfp4(x, wq, ws, wg, ids, out_dtype)
-    if ids is None:
-        _need(x.dim() == 2 and wg.numel() == 1, "need x [m, k] and wg of one element")
-        y = x.new_empty((x.shape[0], n), dtype=out_dtype)
-        _check(load().fpq_gemv_nvfp4(x.data_ptr(), x.shape[0], wq.data_ptr(), ws.data_ptr(), wg.data_ptr(), n, k,
-                                     y.data_ptr(), c_type, _stream(None)), "fpq_gemv_nvfp4")
-        return y
-    _need(ids.dtype is torch.int32 and ids.dim() == 2, "need ids int32 [tokens, topk]")
-    experts, (tokens, topk) = wq.shape[0], ids.shape
-    _need(wg.shape == (experts,), "need wg [E]")
-    _need(x.shape in ((tokens, k), (tokens, topk, k)), "need x [tokens, k] or [tokens, topk, k]")
-    y = x.new_empty((tokens, topk, n), dtype=out_dtype)
-    _check(load().fpq_moe_gemv_nvfp4(x.data_ptr(), x.dim() == 3, ids.data_ptr(), tokens, topk, experts, wq.data_ptr(),
-                                     ws.data_ptr(), wg.data_ptr(), n, k, y.data_ptr(), c_type, _stream(None)),
-           "fpq_moe_gemv_nvfp4")
-    return y
+    return _ops().gemv_nvfp4(x, wq, ws, wg, ids, out_dtype)

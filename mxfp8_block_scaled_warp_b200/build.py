@@ -1,4 +1,5 @@
-"""Build the CUDA library libfpq.so in-tree for sm_100a (nvcc, no JIT cache).
+"""Build the CUDA library libfpq.so in-tree for sm_100a (nvcc, no JIT cache),
+and the Python module _fpq_torch.so over it (g++, torch's headers).
 
     python -m mxfp8_block_scaled_warp_b200.build [--force] [--verbose-ptxas]
 """
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 OBJ_DIR = os.path.join(ROOT, "_build", "fpq")
 LIB = os.path.join(HERE, "libfpq.so")
+TORCH_OPS = os.path.join(HERE, "_fpq_torch.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -85,7 +87,30 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_torch_ops(force)
     return LIB
+
+
+def _build_torch_ops(force: bool) -> None:
+    src = os.path.join(CSRC, "torch_ops.cpp")
+    if not force and not _stale(TORCH_OPS, [src] + _headers()):
+        return
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = TORCH_OPS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], src,
+           "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python", "-L", HERE, "-l:libfpq.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_OPS)
 
 
 def main() -> None:

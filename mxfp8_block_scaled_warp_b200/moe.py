@@ -32,9 +32,9 @@ from typing import NamedTuple
 import torch
 import torch.distributed as dist
 
-from . import (MOE_DIRECT, MOE_PACK, MOE_SIGMOID, MOE_SOFTMAX, _addr, _check, _contiguous, _elsewhere, _need,
-               _out_type, _stream, fpq_moe_dispatch_layout, fpq_moe_dispatch_mxfp8, fpq_moe_pair_rows,
-               fpq_moe_regroup, fpq_moe_route, fpq_moe_route_workspace_bytes, load)
+from . import (MOE_DIRECT, MOE_PACK, MOE_SIGMOID, MOE_SOFTMAX, _on_stream, _ops, fpq_moe_dispatch_layout,
+               fpq_moe_dispatch_mxfp8, fpq_moe_pair_rows, fpq_moe_regroup, fpq_moe_route,
+               fpq_moe_route_workspace_bytes)
 
 __all__ = ["Dispatched", "route", "dispatch", "split_sizes", "exchange_rows", "SOFTMAX", "SIGMOID", "gate",
            "gate_backward", "combine", "combine_backward"]
@@ -186,52 +186,20 @@ def gate(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = None, scor
     with the largest sums of their `group_top` best are chosen.  `renormalize`
     makes a token's weights sum to `scale`.  Equal keys go to the lowest
     index, and ties are judged exactly (fpq_moe_gate in include/fpq.h)."""
-    _need(logits.dim() == 2, "need logits [tokens, E]")
-    kind = _out_type(logits.dtype)
-    tokens, experts = logits.shape
-    _need(bias is None or (bias.dtype is torch.float32 and bias.shape == (experts,)), "need bias fp32 [E]")
-    _contiguous(logits, bias)
-    where = _elsewhere(stream, logits, bias)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, logits):
             return gate(logits, topk, bias, score, n_group, topk_group, group_top, renormalize, scale)
-    ids = logits.new_empty((tokens, topk), dtype=torch.int32)
-    weights = logits.new_empty((tokens, topk), dtype=torch.float32)
-    _check(load().fpq_moe_gate(logits.data_ptr(), kind, _addr(bias), tokens, experts, score, n_group, topk_group,
-                               group_top, topk, renormalize, scale, ids.data_ptr(), weights.data_ptr(),
-                               _stream(None)), "fpq_moe_gate")
-    return ids, weights
+    return _ops().moe_gate(logits, topk, bias, score, n_group, topk_group, group_top, renormalize, scale)
 
 
 def gate_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: int = SOFTMAX,
                   renormalize: bool = True, scale: float = 1.0, stream=None):
     """Gradient of the logits (their type and shape) for the gradient dweights
     fp32 [tokens, topk] of gate's weights, with the ids that gate chose."""
-    _need(logits.dim() == 2, "need logits [tokens, E]")
-    kind = _out_type(logits.dtype)
-    tokens, experts = logits.shape
-    _need(ids.dtype is torch.int32 and ids.dim() == 2 and ids.shape[0] == tokens, "need ids int32 [tokens, topk]")
-    _need(dweights.dtype is torch.float32 and dweights.shape == ids.shape, "need dweights fp32 of ids' shape")
-    _contiguous(logits, ids, dweights)
-    where = _elsewhere(stream, logits, ids, dweights)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, logits):
             return gate_backward(dweights, logits, ids, score, renormalize, scale)
-    dlogits = torch.empty_like(logits)
-    _check(load().fpq_moe_gate_backward(logits.data_ptr(), kind, ids.data_ptr(), dweights.data_ptr(), tokens, experts,
-                                        score, ids.shape[1], renormalize, scale, dlogits.data_ptr(), _stream(None)),
-           "fpq_moe_gate_backward")
-    return dlogits
-
-
-def _pairs(y, weights, rows):
-    """(rows of y, hidden) after the checks that combine and its backward share."""
-    _need(weights.dtype is torch.float32 and weights.dim() == 2, "need weights fp32 [tokens, topk]")
-    _need(y.dim() == 2 or (y.dim() == 3 and rows is None and y.shape[:2] == weights.shape),
-          "need y [rows, hidden], or [tokens, topk, hidden] without a row map")
-    _need(rows is None or (rows.dtype == torch.int32 and rows.shape == weights.shape),
-          "need rows int32 of weights' shape")
-    return y.shape[:-1].numel(), y.shape[-1]
+    return _ops().moe_gate_backward(dweights, logits, ids, score, renormalize, scale)
 
 
 def combine(y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = None,
@@ -241,20 +209,10 @@ def combine(y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = 
     the map that dispatch fills in (-1: a dropped pair); without it y is
     [tokens, topk, hidden] (or the same rows in two dimensions).  `add`: bf16
     [tokens, hidden], a shared expert's output for instance."""
-    y_rows, hidden = _pairs(y, weights, rows)
-    tokens, topk = weights.shape
-    _need(add is None or (add.dtype == torch.bfloat16 and add.shape == (tokens, hidden)),
-          "need add bf16 [tokens, hidden]")
-    kind, out_kind = _out_type(y.dtype), _out_type(out_dtype)
-    _contiguous(y, weights, rows, add)
-    where = _elsewhere(stream, y, weights, rows, add)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, y):
             return combine(y, weights, rows, add, out_dtype)
-    out = y.new_empty((tokens, hidden), dtype=out_dtype)
-    _check(load().fpq_moe_combine(y.data_ptr(), kind, y_rows, _addr(rows), weights.data_ptr(), tokens, topk, hidden,
-                                  _addr(add), out.data_ptr(), out_kind, _stream(None)), "fpq_moe_combine")
-    return out
+    return _ops().moe_combine(y, weights, rows, add, out_dtype)
 
 
 def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, rows: torch.Tensor | None = None,
@@ -264,20 +222,7 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor,
     topk]); add's gradient is dout itself.  Rows of dy that no pair names are
     left as they were in the buffer (`dy`, or a new one).  A row may be named
     by one pair only."""
-    y_rows, hidden = _pairs(y, weights, rows)
-    tokens, topk = weights.shape
-    _need(dout.shape == (tokens, hidden), "need dout [tokens, hidden]")
-    _need(dy is None or (dy.dtype == y.dtype and dy.shape == y.shape), "need dy of y's type and shape")
-    kind, d_kind = _out_type(y.dtype), _out_type(dout.dtype)
-    _contiguous(dout, y, weights, rows, dy)
-    where = _elsewhere(stream, y, dout, weights, rows, dy)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, y):
             return combine_backward(dout, y, weights, rows, dy)
-    if dy is None:
-        dy = torch.empty_like(y)
-    dweights = torch.empty_like(weights)
-    _check(load().fpq_moe_combine_backward(dout.data_ptr(), d_kind, y.data_ptr(), kind, y_rows, _addr(rows),
-                                           weights.data_ptr(), tokens, topk, hidden, dy.data_ptr(),
-                                           dweights.data_ptr(), _stream(None)), "fpq_moe_combine_backward")
-    return dy, dweights
+    return _ops().moe_combine_backward(dout, y, weights, rows, dy)
