@@ -22,10 +22,15 @@
 // whose chosen scores sum to 0 gets zero weights.
 //
 // One warp per token, expert e = 32 i + lane in register i: the row is read
-// once, coalesced, and every step is a warp reduction.  The traffic (a
-// logit read per expert) is a few microseconds at most; what bounds the
-// kernel is the chain of topk dependent reductions per token, hidden by the
-// other warps of the SM.
+// once, coalesced.  The traffic (a logit read per expert) is a few
+// microseconds at most; what bounds the kernel is its instructions, about
+// 200 per token and 64 experts.  So the topk largest are not taken one after
+// the other: the topk-th largest of the 32 lane maxima bounds them from
+// below, the few keys at or above it (ten for eight of 256) are gathered, one
+// per lane, and each counts how many are before it, which is its place in
+// the output.  (Taking one maximum after the other: 51 us instead of the
+// figure below for 16384 tokens, 256 experts in groups; it remains for rows
+// with more than 32 such keys, which take equal logits.)
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -68,6 +73,8 @@ template <> __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+// For keys: within 2^-20, what `slack` allows for.
+__device__ __forceinline__ float sigmoid_key(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -122,6 +129,7 @@ template <typename T, bool SIGMOID, int VPT>
 __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_kernel(const GateArgs a) {
     extern __shared__ float sh[];                           // per warp: keys of the row, padded per 32 (groups only)
+    __shared__ uint2 gathered[kGateWarps][32];               // key pattern, expert
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
@@ -133,7 +141,8 @@ moe_gate_kernel(const GateArgs a) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) l[i] = 32 * i + lane < E ? load_logit<T>(row + 32 * i + lane) : -INFINITY;
 
-    // softmax maximum and sum, where the scores themselves are needed
+    // softmax maximum and sum, where the scores themselves are needed (the
+    // weights take the sum only without renormalize)
     const bool scores = a.bias || a.n_group > 1;
     float mx = -INFINITY, sum = 0.0f;
     if (!SIGMOID && (scores || !a.renormalize)) {
@@ -142,14 +151,15 @@ moe_gate_kernel(const GateArgs a) {
         mx = warp_max(mx);
         if (mx != -INFINITY) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) sum += 32 * i + lane < E ? expf(l[i] - mx) : 0.0f;
+            for (int i = 0; i < VPT; ++i)
+                sum += 32 * i + lane < E ? (a.renormalize ? __expf(l[i] - mx) : expf(l[i] - mx)) : 0.0f;
             sum = warp_sum(sum);
         }
     }
-    const auto score = [&](float x) {
-        if (SIGMOID) return sigmoid(x);
+    const auto score_key = [&](float x) {
+        if (SIGMOID) return sigmoid_key(x);
         if (mx == -INFINITY) return x == x ? 0.0f : x;
-        return __fdiv_rn(expf(x - mx), sum);
+        return __fdividef(__expf(x - mx), sum);
     };
     double sum64 = 0.0;
     const auto need64 = [&]() {                             // warp-uniform
@@ -168,7 +178,7 @@ moe_gate_kernel(const GateArgs a) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int e = 32 * i + lane;
-        key[i] = e >= E ? kTaken : pattern(a.bias ? score(l[i]) + __ldg(a.bias + e) : l[i]);
+        key[i] = e >= E ? kTaken : pattern(a.bias ? score_key(l[i]) + __ldg(a.bias + e) : l[i]);
     }
 
     if (a.n_group > 1) {
@@ -176,40 +186,48 @@ moe_gate_kernel(const GateArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = 32 * i + lane;
-            if (e < E) s[e + i] = a.bias ? value(key[i]) : score(l[i]);
+            if (e < E) s[e + i] = a.bias ? value(key[i]) : score_key(l[i]);
         }
         __syncwarp();
-        const int size = E / a.n_group;
-        // rank of group `lane`: its largest key, or its two largest
+        // `split` adjacent lanes share a group; lane `split` g holds its rank:
+        // its largest key, or the sum of its two largest
+        const int size = E / a.n_group, split = 32 >> (32 - __clz(a.n_group - 1)), g = lane / split;
         float first = -INFINITY, second = -INFINITY;
-        if (lane < a.n_group)
-            for (int e = lane * size; e < (lane + 1) * size; ++e) {
+        if (g < a.n_group)
+#pragma unroll 4
+            for (int e = g * size + lane % split; e < (g + 1) * size; e += split) {
                 const float v = s[e + (e >> 5)];
-                if (v > first) { second = first; first = v; }
-                else if (v > second) second = v;
+                second = fmaxf(second, fminf(first, v));    // a NaN is passed over
+                first = fmaxf(first, v);
             }
+        for (int o = 1; o < split; o <<= 1) {
+            const float f = __shfl_xor_sync(kFull, first, o), n = __shfl_xor_sync(kFull, second, o);
+            second = fmaxf(fmaxf(second, n), fminf(first, f));
+            first = fmaxf(first, f);
+        }
         const float rank = a.group_top == 2 ? first + second : first;
-        uint32_t gkey = lane < a.n_group ? pattern(rank) : kTaken;
+        const bool holds = g < a.n_group && lane % split == 0;
+        uint32_t gkey = holds ? pattern(rank) : kTaken;
         uint32_t open = 0;                                   // chosen groups
-        for (int g = 0; g < a.topk_group; ++g) {
+        for (int c = 0; c < a.topk_group; ++c) {
             const uint32_t m = __reduce_max_sync(kFull, gkey);
             const float least = value(m) - slack(value(m), a.group_top);
             const bool near = gkey != kTaken && (gkey == m || (gkey > kNaN && value(gkey) >= least));
-            uint32_t cand = __ballot_sync(kFull, near);
+            const uint32_t cand = __ballot_sync(kFull, near);
             int best = __ffs(cand) - 1;
             if (cand & (cand - 1)) {
                 need64();
                 double f = -INFINITY, n = -INFINITY;
                 if (near)
 #pragma unroll 1
-                    for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                    for (int e = g * size; e < (g + 1) * size; ++e) {
                         const double v = key64(e);
                         if (v > f) { n = f; f = v; }
                         else if (v > n) n = v;
                     }
                 best = best64(a.group_top == 2 ? f + n : f, lane, near);
             }
-            open |= 1u << best;
+            open |= 1u << (best / split);
             if (lane == best) gkey = kTaken;
         }
 #pragma unroll
@@ -219,20 +237,79 @@ moe_gate_kernel(const GateArgs a) {
         }
     }
 
-    int mine = 0;                                            // lane j keeps choice j
-    for (int j = 0; j < a.topk; ++j) {
-        uint32_t top = key[0];
+    // the topk-th largest lane maximum (or below it: equal ones count at once)
+    uint32_t top = key[0];
 #pragma unroll
-        for (int i = 1; i < VPT; ++i) top = max(top, key[i]);
-        const uint32_t m = __reduce_max_sync(kFull, top);
-        int best;
-        bool resolved = false;
-        if (a.bias && m > kNaN) {
-            const uint32_t least = pattern(value(m) - slack(value(m), 1));
-            int count = 0;
+    for (int i = 1; i < VPT; ++i) top = max(top, key[i]);
+    uint32_t bound = 0;
+    for (int have = 0; have < a.topk;) {
+        bound = __reduce_max_sync(kFull, top);
+        const uint32_t equal = __ballot_sync(kFull, top == bound);
+        have += __popc(equal);
+        if (bound == kTaken) break;
+        if (top == bound) top = kTaken;
+    }
+    if (a.bias && bound > kNaN) bound = pattern(value(bound) - slack(value(bound), 1));
+    bound = max(bound, kNaN);                                // there are topk experts inside the chosen groups
+    int count = 0;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) count += key[i] >= least;
-            if (__reduce_add_sync(kFull, (unsigned)count) > 1) {
+    for (int i = 0; i < VPT; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t mask = __ballot_sync(kFull, in);
+        const int at = count + __popc(mask & ((1u << lane) - 1u));
+        if (in && at < 32) gathered[warp][at] = make_uint2(key[i], (uint32_t)(32 * i + lane));
+        count += __popc(mask);
+    }
+    __syncwarp();
+
+    int mine = 0, place = 32;                                // this lane's expert and its place in the output
+    if (count <= 32) {
+        // in order of the expert's index: an equal key before this one's goes first
+        const uint2 c = lane < count ? gathered[warp][lane] : make_uint2(kTaken, 0);
+        mine = (int)c.y;
+        place = lane < count ? 0 : 32;
+        bool near = false;
+        if (a.bias) {
+            const float v = value(c.x), reach = slack(v, 1);
+            for (int j = 0; j < count; ++j) {
+                const uint32_t k = __shfl_sync(kFull, c.x, j);
+                place += (k > c.x || (k == c.x && j < lane)) ? 1 : 0;
+                near |= j != lane && c.x > kNaN && k > kNaN && fabsf(value(k) - v) <= reach;
+            }
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < count; ++j) {
+                const uint32_t k = __shfl_sync(kFull, c.x, j);
+                place += (k > c.x || (k == c.x && j < lane)) ? 1 : 0;
+            }
+        }
+        if (__any_sync(kFull, near && lane < count)) {
+            need64();
+            double k64 = lane < count ? key64(mine) : 0.0;
+            if (!(k64 == k64)) k64 = -INFINITY;
+            // NaN patterns are behind every number
+            const int group = c.x > kNaN;
+            place = lane < count ? 0 : 32;
+            for (int j = 0; j < count; ++j) {
+                const double k = __shfl_sync(kFull, k64, j);
+                const int other = __shfl_sync(kFull, group, j);
+                place += (other > group || (other == group && (k > k64 || (k == k64 && j < lane)))) ? 1 : 0;
+            }
+        }
+    } else {
+        // one maximum after the other
+        for (int j = 0; j < a.topk; ++j) {
+            uint32_t t = key[0];
+#pragma unroll
+            for (int i = 1; i < VPT; ++i) t = max(t, key[i]);
+            const uint32_t m = __reduce_max_sync(kFull, t);
+            uint32_t least = m;
+            if (a.bias && m > kNaN) least = pattern(value(m) - slack(value(m), 1));
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) n += key[i] >= least;
+            int best;
+            if (least < m && __reduce_add_sync(kFull, (unsigned)n) > 1) {
                 need64();
                 double bk = -INFINITY;
                 int be = 0;
@@ -244,31 +321,34 @@ moe_gate_kernel(const GateArgs a) {
                         if (!has || k > bk) { bk = k; be = 32 * i + lane; has = true; }
                     }
                 best = best64(bk, be, has);
-                resolved = true;
+            } else {
+                uint32_t e = 0xFFFFFFFFu;
+#pragma unroll
+                for (int i = VPT - 1; i >= 0; --i)
+                    if (key[i] == m) e = 32 * i + lane;
+                best = (int)__reduce_min_sync(kFull, e);
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (32 * i + lane == best) key[i] = kTaken;
+            if (lane == j) {
+                mine = best;
+                place = j;
             }
         }
-        if (!resolved) {
-            uint32_t e = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = VPT - 1; i >= 0; --i)
-                if (key[i] == m) e = 32 * i + lane;
-            best = (int)__reduce_min_sync(kFull, e);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (32 * i + lane == best) key[i] = kTaken;
-        if (lane == j) mine = best;
     }
 
-    // weights of the chosen experts, choice j in lane j
-    const bool have = lane < a.topk;
+    // weights of the chosen experts
+    const bool have = place < a.topk;
     const float x = have ? load_logit<T>(row + mine) : -INFINITY;
     float p;
-    if (!SIGMOID && a.renormalize) {                         // softmax over the chosen logits
+    if (SIGMOID) {
+        p = sigmoid(x);
+    } else if (a.renormalize) {                              // softmax over the chosen logits
         const float cm = warp_max(x);
         p = cm == -INFINITY && !(x != x) ? 0.0f : expf(x - cm);
     } else {
-        p = score(x);
+        p = mx == -INFINITY ? (x == x ? 0.0f : x) : __fdiv_rn(expf(x - mx), sum);
     }
     if (!have) p = 0.0f;
     if (a.renormalize) {
@@ -276,8 +356,118 @@ moe_gate_kernel(const GateArgs a) {
         p = total == 0.0f ? 0.0f : __fdiv_rn(p, total);
     }
     if (have) {
-        a.ids[tok * a.topk + lane] = mine;
-        a.weights[tok * a.topk + lane] = p * a.scale;
+        a.ids[tok * a.topk + place] = mine;
+        a.weights[tok * a.topk + place] = p * a.scale;
+    }
+}
+
+// Up to eight of few experts, without a bias: LANES lanes per token, expert
+// e = LANES i + s in register i of the token's lane s, 32 / LANES tokens per
+// warp.  Each lane sorts its eight keys, and log2 LANES times two lanes merge
+// their lists: the larger of element i of one and 7 - i of the other are the
+// eight largest of both, in bitonic order.  No step waits for the one before
+// as in taking maxima one after the other, and the four tokens of a warp
+// share the instructions: 40 per token for 64 bf16 logits.  A key carries its
+// index, so that equal logits compare by it: in the lower half of a bf16
+// logit's pattern (which is the type's own width), else in a second word.
+template <int LANES, typename T> struct MergeKey;
+template <int LANES> struct MergeKey<LANES, uint16_t> {
+    using K = uint32_t;
+    // NaN (2) becomes 0, below -inf (0x007F....)
+    static __device__ __forceinline__ K make(uint32_t p, int e) { return (p & 0xFFFF0000u) | (uint32_t)(8 * LANES - e); }
+    static __device__ __forceinline__ int index(K k) { return 8 * LANES - (int)(k & 0xFFFFu); }
+};
+template <int LANES> struct MergeKey<LANES, float> {
+    using K = unsigned long long;
+    static __device__ __forceinline__ K make(uint32_t p, int e) { return ((K)p << 32) | (uint32_t)(8 * LANES - e); }
+    static __device__ __forceinline__ int index(K k) { return 8 * LANES - (int)(uint32_t)k; }
+};
+
+template <typename K>
+__device__ __forceinline__ void order2(K& hi, K& lo) {
+    const K a = hi, b = lo;
+    hi = max(a, b);
+    lo = min(a, b);
+}
+
+template <typename T, bool SIGMOID, int LANES>
+__global__ void __launch_bounds__(32 * kGateWarps)
+moe_gate_merge_kernel(const GateArgs a) {
+    using M = MergeKey<LANES, T>;
+    using K = typename M::K;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, s = lane % LANES, E = a.experts;
+    const int64_t tok = ((int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * (32 / LANES) + lane / LANES;
+    const bool live = tok < a.tokens;                        // the warp's other tokens go on
+    const T* row = static_cast<const T*>(a.logits) + (live ? tok : 0) * E;
+    float l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = LANES * i + s < E ? load_logit<T>(row + LANES * i + s) : -INFINITY;
+    float mx = -INFINITY, sum = 0.0f;
+    if (!SIGMOID && !a.renormalize) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, l[i]);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        if (mx != -INFINITY)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += LANES * i + s < E ? expf(l[i] - mx) : 0.0f;
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    }
+    K k[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = LANES * i + s < E ? M::make(pattern(l[i]), LANES * i + s) : (K)0;
+    // Batcher's network for eight
+    order2(k[0], k[1]); order2(k[2], k[3]); order2(k[4], k[5]); order2(k[6], k[7]);
+    order2(k[0], k[2]); order2(k[1], k[3]); order2(k[4], k[6]); order2(k[5], k[7]);
+    order2(k[1], k[2]); order2(k[5], k[6]);
+    order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
+    order2(k[2], k[4]); order2(k[3], k[5]);
+    order2(k[1], k[2]); order2(k[3], k[4]); order2(k[5], k[6]);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+        K other[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kFull, k[7 - i], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = max(k[i], other[i]);
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((i & d) == 0) order2(k[i], k[i + d]);
+    }
+    // every lane holds the token's list; lane j < topk takes choice j
+    K own = k[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+        if (s == j) own = k[j];
+    const bool have = live && s < a.topk;
+    const int mine = M::index(own);
+    const float x = have ? load_logit<T>(row + mine) : -INFINITY;
+    float p;
+    if (SIGMOID) {
+        p = sigmoid(x);
+    } else if (a.renormalize) {                              // softmax over the chosen logits
+        float cm = x;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(kFull, cm, o));
+        p = cm == -INFINITY && !(x != x) ? 0.0f : expf(x - cm);
+    } else {
+        p = mx == -INFINITY ? (x == x ? 0.0f : x) : __fdiv_rn(expf(x - mx), sum);
+    }
+    if (!have) p = 0.0f;
+    if (a.renormalize) {
+        float total = p;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+        p = total == 0.0f ? 0.0f : __fdiv_rn(p, total);
+    }
+    if (have) {
+        a.ids[tok * a.topk + s] = mine;
+        a.weights[tok * a.topk + s] = p * a.scale;
     }
 }
 
@@ -392,6 +582,19 @@ cudaError_t gate(const GateArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)((a.tokens + kGateWarps - 1) / kGateWarps)), block(32 * kGateWarps);
     const size_t smem = a.n_group > 1 ? (size_t)kGateWarps * (a.experts + a.experts / 32 + 1) * sizeof(float) : 0;
     const int E = a.experts;
+    // Merging lists: without a bias, up to eight choices; 256 bf16 logits, 64
+    // fp32 ones (whose two-word keys cost three times the instructions).
+    if (!a.bias && a.n_group == 1 && a.topk <= 8 && E <= (sizeof(T) == 2 ? 256 : 64)) {
+        const auto merge = [&](auto kernel, int lanes) {
+            const int64_t per = kGateWarps * 32 / lanes;
+            return launch_pdl(kernel, dim3((unsigned)((a.tokens + per - 1) / per)), block, 0, st, a);
+        };
+        if (E <= 64) return merge(moe_gate_merge_kernel<T, SIGMOID, 8>, 8);
+        if constexpr (sizeof(T) == 2) {
+            if (E <= 128) return merge(moe_gate_merge_kernel<T, SIGMOID, 16>, 16);
+            return merge(moe_gate_merge_kernel<T, SIGMOID, 32>, 32);
+        }
+    }
     if (E <= 32) return launch_pdl(moe_gate_kernel<T, SIGMOID, 1>, grid, block, smem, st, a);
     if (E <= 64) return launch_pdl(moe_gate_kernel<T, SIGMOID, 2>, grid, block, smem, st, a);
     if (E <= 128) return launch_pdl(moe_gate_kernel<T, SIGMOID, 4>, grid, block, smem, st, a);
