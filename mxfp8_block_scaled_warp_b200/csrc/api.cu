@@ -611,7 +611,7 @@ fpq_status fpq_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, con
         return FPQ_ERR_WORKSPACE;
     }
     return from_cuda(fpq::launch_rmsnorm_backward(dy, x, ld_x, weight, rstd, dres, rows, cols, dx, dweight, workspace,
-                                                  d->sms, (cudaStream_t)stream),
+                                                  d->err, d->sms, (cudaStream_t)stream),
                      "rmsnorm backward launch");
 }
 
@@ -743,7 +743,7 @@ fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype, const 
     if (!d) return st;
     return from_cuda(fpq::launch_moe_combine_backward(dout, dout_dtype == FPQ_OUT_F32, y, y_dtype == FPQ_OUT_F32,
                                                       y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
-                                                      d->err, (cudaStream_t)stream),
+                                                      d->err, d->sms, (cudaStream_t)stream),
                      "moe combine backward launch");
 }
 

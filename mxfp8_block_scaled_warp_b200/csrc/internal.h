@@ -116,7 +116,7 @@ cudaError_t launch_rmsnorm_quantize(int fmt, const void* x, int64_t ld_x, const 
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, int sms);
 cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight,
                                     const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
-                                    float* dweight, void* workspace, int sms, cudaStream_t st);
+                                    float* dweight, void* workspace, uint32_t* err, int sms, cudaStream_t st);
 
 // Expert gate (moe_gate.cu): f32 selects fp32 logits, else bf16.
 cudaError_t launch_moe_gate(const void* logits, int f32, const float* bias, int64_t tokens, int experts, int sigmoid,
@@ -135,7 +135,8 @@ cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const i
                                uint32_t* err, cudaStream_t st);
 cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
                                         const int32_t* rows, const float* weights, int64_t tokens, int topk,
-                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, cudaStream_t st);
+                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, int sms,
+                                        cudaStream_t st);
 
 // Few rows times NVFP4 weights (gemv_nvfp4.cu): row m of y [m, n] is row
 // m / x_div of x times the matrix (ids == nullptr) or expert ids[m]'s.

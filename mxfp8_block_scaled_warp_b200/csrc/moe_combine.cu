@@ -12,8 +12,10 @@
 // writer and a fixed order of additions.
 //
 // Bound by HBM: the forward reads topk rows and writes one per token, the
-// backward reads and writes topk rows.  Every thread keeps the loads of up
-// to eight rows' vectors in flight.
+// backward reads and writes topk rows.  A thread keeps eight loads of 16
+// bytes in flight: one vector of eight rows, two of four or four of two.
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -23,7 +25,7 @@ namespace fpq {
 
 namespace {
 
-constexpr int kBatch = 8;                 // rows in flight per thread
+constexpr int kInFlight = 8;              // vectors per thread: KB rows of kInFlight / KB vectors each
 constexpr int kCombineThreads = 256;
 
 // Eight consecutive elements as fp32; index in units of eight.
@@ -80,48 +82,60 @@ __device__ __forceinline__ int64_t pair_row(const CombineArgs& a, int64_t p, boo
     return -1;
 }
 
-// CTA (x, y): vectors [256 y, 256 y + 256) of token x's row.
-template <bool Y32, bool OUT32>
+// CTA (x, y): the y-th part of token x's row, kInFlight / KB vectors per thread.
+template <bool Y32, bool OUT32, int KB>
 __global__ void __launch_bounds__(kCombineThreads)
 moe_combine_kernel(const CombineArgs a) {
+    constexpr int VB = kInFlight / KB;
     pdl_trigger();
     pdl_wait();
     const int64_t tok = blockIdx.x;
-    const int v = blockIdx.y * blockDim.x + threadIdx.x;
-    if (v >= a.nvec) return;
-    float acc[8];
-    if (a.add) {
-        Vec8<false> u;
-        u.load(a.add, tok * a.nvec + v);
-        u.get(acc);
-    } else {
+    const int v0 = blockIdx.y * blockDim.x * VB + threadIdx.x, step = blockDim.x;
+    if (v0 >= a.nvec) return;
+    float acc[VB][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < VB; ++i) {
+        if (a.add && v0 + i * step < a.nvec) {
+            Vec8<false> u;
+            u.load(a.add, tok * a.nvec + v0 + i * step);
+            u.get(acc[i]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[i][c] = 0.0f;
+        }
     }
-    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
-        Vec8<Y32> u[kBatch];
-        float w[kBatch];
-        bool ok[kBatch];
+    for (int j0 = 0; j0 < a.topk; j0 += KB) {
+        Vec8<Y32> u[KB][VB];
+        float w[KB];
+        bool ok[KB];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < KB; ++j) {
             ok[j] = j0 + j < a.topk;
             if (!ok[j]) continue;
             const int64_t p = tok * a.topk + j0 + j, r = pair_row(a, p, threadIdx.x == 0);
             ok[j] = r >= 0;
             if (!ok[j]) continue;
             w[j] = __ldg(a.weights + p);
-            u[j].load(a.y, r * a.nvec + v);
+#pragma unroll
+            for (int i = 0; i < VB; ++i)
+                if (v0 + i * step < a.nvec) u[j][i].load(a.y, r * a.nvec + v0 + i * step);
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < KB; ++j) {
             if (!ok[j]) continue;
-            float f[8];
-            u[j].get(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+            for (int i = 0; i < VB; ++i) {
+                if (v0 + i * step >= a.nvec) continue;
+                float f[8];
+                u[j][i].get(f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) acc[i][c] = fmaf(w[j], f[c], acc[i][c]);
+            }
         }
     }
-    Vec8<OUT32>::store(a.out, tok * a.nvec + v, acc);
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+        if (v0 + i * step < a.nvec) Vec8<OUT32>::store(a.out, tok * a.nvec + v0 + i * step, acc[i]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -130,60 +144,82 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One CTA per token: dout's vectors are read once per eight choices (from L1
-// after the first), each y vector once; the dots are reduced at the end.
-template <bool Y32, bool D32>
+// A token per warp where there are many (no barrier), else per CTA.  dout's
+// vectors are read once per KB choices (from L1 after the first), each y
+// vector once; the dots are reduced at the end.
+template <bool Y32, bool D32, int KB, bool WARP>
 __global__ void __launch_bounds__(kCombineThreads)
 moe_combine_bwd_kernel(const CombineArgs a) {
-    __shared__ float red[kCombineThreads / 32][kBatch];
+    constexpr int VB = kInFlight / KB;
+    __shared__ float red[kCombineThreads / 32][KB];
     pdl_trigger();
     pdl_wait();
-    const int64_t tok = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
-        int64_t r[kBatch];
-        float w[kBatch], dot[kBatch];
+    const int64_t tok = WARP ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
+    if (tok >= a.tokens) return;                             // whole warps; with a CTA per token never
+    const int t = WARP ? lane : threadIdx.x, T = WARP ? 32 : blockDim.x;
+    for (int j0 = 0; j0 < a.topk; j0 += KB) {
+        int64_t r[KB];
+        float w[KB], dot[KB];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < KB; ++j) {
             const int64_t p = tok * a.topk + j0 + j;
-            r[j] = j0 + j < a.topk ? pair_row(a, p, threadIdx.x == 0) : -1;
+            r[j] = j0 + j < a.topk ? pair_row(a, p, t == 0) : -1;
             w[j] = r[j] >= 0 ? __ldg(a.weights + p) : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) {
-            Vec8<D32> d;
-            Vec8<Y32> u[kBatch];
-            d.load(a.dout, tok * a.nvec + v);
+        for (int v0 = t; v0 < a.nvec; v0 += T * VB) {
+            Vec8<D32> d[VB];
+            Vec8<Y32> u[KB][VB];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (r[j] >= 0) u[j].load(a.y, r[j] * a.nvec + v);
-            float df[8];
-            d.get(df);
+            for (int i = 0; i < VB; ++i) {
+                const int v = v0 + i * T;
+                if (v >= a.nvec) continue;
+                d[i].load(a.dout, tok * a.nvec + v);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (r[j] < 0) continue;
-                float f[8];
-                u[j].get(f);
+                for (int j = 0; j < KB; ++j)
+                    if (r[j] >= 0) u[j][i].load(a.y, r[j] * a.nvec + v);
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot[j] = fmaf(df[i], f[i], dot[j]);
-                    f[i] = w[j] * df[i];
+            for (int i = 0; i < VB; ++i) {
+                const int v = v0 + i * T;
+                if (v >= a.nvec) continue;
+                float df[8];
+                d[i].get(df);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    if (r[j] < 0) continue;
+                    float f[8];
+                    u[j][i].get(f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        dot[j] = fmaf(df[c], f[c], dot[j]);
+                        f[c] = w[j] * df[c];
+                    }
+                    Vec8<Y32>::store(a.out, r[j] * a.nvec + v, f);
                 }
-                Vec8<Y32>::store(a.out, r[j] * a.nvec + v, f);
             }
         }
+        if (WARP) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const float s = warp_sum(dot[j]);
-            if (lane == 0) red[warp][j] = s;
+            for (int j = 0; j < KB; ++j) {
+                const float s = warp_sum(dot[j]);
+                if (lane == 0 && j0 + j < a.topk) a.dweights[tok * a.topk + j0 + j] = s;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const float s = warp_sum(dot[j]);
+                if (lane == 0) red[warp][j] = s;
+            }
+            __syncthreads();
+            if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.topk) {
+                float s = 0.0f;
+                for (int i = 0; i < warps; ++i) s += red[i][threadIdx.x];
+                a.dweights[tok * a.topk + j0 + threadIdx.x] = s;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < a.topk) {
-            float s = 0.0f;
-            for (int i = 0; i < warps; ++i) s += red[i][threadIdx.x];
-            a.dweights[tok * a.topk + j0 + threadIdx.x] = s;
-        }
-        __syncthreads();
     }
 }
 
@@ -234,32 +270,60 @@ cudaError_t launch_moe_pair_rows(const int32_t* ids, int64_t tokens, int topk, i
                       base, tpc, chunks, dst_row0, rows);
 }
 
+namespace {
+
+template <bool Y32, bool OUT32, int KB>
+cudaError_t combine(const CombineArgs& a, cudaStream_t st) {
+    const int per = (a.nvec + kInFlight / KB - 1) / (kInFlight / KB);      // threads that a row takes
+    const int threads = per >= kCombineThreads ? kCombineThreads : (per + 31) / 32 * 32;
+    return launch_pdl(moe_combine_kernel<Y32, OUT32, KB>, dim3((unsigned)a.tokens, (unsigned)((per + threads - 1) / threads)),
+                      dim3((unsigned)threads), 0, st, a);
+}
+
+template <bool Y32, bool D32, int KB>
+cudaError_t combine_backward(const CombineArgs& a, int sms, cudaStream_t st) {
+    // A warp per token needs tokens for sixteen warps per SM (16000 tokens x
+    // 2048, two choices: WARP 58 us, CTA 152 us); with fewer, a CTA per token
+    // is done sooner (16 tokens x 7168, eight choices: 5.5 us instead of 24).
+    if (a.tokens >= 16 * (int64_t)sms)
+        return launch_pdl(moe_combine_bwd_kernel<Y32, D32, KB, true>,
+                          dim3((unsigned)((a.tokens + kCombineThreads / 32 - 1) / (kCombineThreads / 32))),
+                          dim3(kCombineThreads), 0, st, a);
+    const int threads = a.nvec >= kCombineThreads ? kCombineThreads : (a.nvec + 31) / 32 * 32;
+    return launch_pdl(moe_combine_bwd_kernel<Y32, D32, KB, false>, dim3((unsigned)a.tokens), dim3((unsigned)threads), 0,
+                      st, a);
+}
+
+template <typename F>
+cudaError_t by_types(bool y32, bool o32, int topk, F&& f) {
+    const auto by_topk = [&](auto y, auto o) {
+        if (topk <= 2) return f(y, o, std::integral_constant<int, 2>());
+        if (topk <= 4) return f(y, o, std::integral_constant<int, 4>());
+        return f(y, o, std::integral_constant<int, 8>());
+    };
+    if (y32) return o32 ? by_topk(std::true_type(), std::true_type()) : by_topk(std::true_type(), std::false_type());
+    return o32 ? by_topk(std::false_type(), std::true_type()) : by_topk(std::false_type(), std::false_type());
+}
+
+}  // namespace
+
 cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const int32_t* rows, const float* weights,
                                int64_t tokens, int topk, int64_t hidden, const void* add, void* out, int out_f32,
                                uint32_t* err, cudaStream_t st) {
-    const int nvec = (int)(hidden / 8);
-    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, nvec, add, nullptr, out, nullptr, err};
-    const int threads = nvec >= kCombineThreads ? kCombineThreads : (nvec + 31) / 32 * 32;
-    const dim3 grid((unsigned)tokens, (unsigned)((nvec + threads - 1) / threads)), block((unsigned)threads);
-    if (y_f32)
-        return out_f32 ? launch_pdl(moe_combine_kernel<true, true>, grid, block, 0, st, a)
-                       : launch_pdl(moe_combine_kernel<true, false>, grid, block, 0, st, a);
-    return out_f32 ? launch_pdl(moe_combine_kernel<false, true>, grid, block, 0, st, a)
-                   : launch_pdl(moe_combine_kernel<false, false>, grid, block, 0, st, a);
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), add, nullptr, out, nullptr, err};
+    return by_types(y_f32 != 0, out_f32 != 0, topk, [&](auto y32, auto o32, auto kb) {
+        return combine<decltype(y32)::value, decltype(o32)::value, decltype(kb)::value>(a, st);
+    });
 }
 
 cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
                                         const int32_t* rows, const float* weights, int64_t tokens, int topk,
-                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, cudaStream_t st) {
-    const int nvec = (int)(hidden / 8);
-    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, nvec, nullptr, dout, dy, dweights, err};
-    const int threads = nvec >= kCombineThreads ? kCombineThreads : (nvec + 31) / 32 * 32;
-    const dim3 grid((unsigned)tokens), block((unsigned)threads);
-    if (y_f32)
-        return dout_f32 ? launch_pdl(moe_combine_bwd_kernel<true, true>, grid, block, 0, st, a)
-                        : launch_pdl(moe_combine_bwd_kernel<true, false>, grid, block, 0, st, a);
-    return dout_f32 ? launch_pdl(moe_combine_bwd_kernel<false, true>, grid, block, 0, st, a)
-                    : launch_pdl(moe_combine_bwd_kernel<false, false>, grid, block, 0, st, a);
+                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, int sms,
+                                        cudaStream_t st) {
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), nullptr, dout, dy, dweights, err};
+    return by_types(y_f32 != 0, dout_f32 != 0, topk, [&](auto y32, auto d32, auto kb) {
+        return combine_backward<decltype(y32)::value, decltype(d32)::value, decltype(kb)::value>(a, sms, st);
+    });
 }
 
 }  // namespace fpq

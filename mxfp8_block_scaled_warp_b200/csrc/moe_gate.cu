@@ -230,10 +230,12 @@ moe_gate_kernel(const GateArgs a) {
             open |= 1u << (best / split);
             if (lane == best) gkey = kTaken;
         }
+        // e / size for e < 1024: the reciprocal is off by less than e / 2^20 < 1 / size
+        const uint32_t inverse = ((1u << 20) + size - 1) / size;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = 32 * i + lane;
-            if (e < E && !((open >> (e / size)) & 1u)) key[i] = kOutside;
+            if (e < E && !((open >> ((e * inverse) >> 20)) & 1u)) key[i] = kOutside;
         }
     }
 

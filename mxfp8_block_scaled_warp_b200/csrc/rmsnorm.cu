@@ -13,15 +13,20 @@
 //   dx = dres + rstd g - x (rstd^3 / cols) sum(g x),   g = dy w
 //   dw = sum over rows of dy x rstd
 //
-// Both are bound by HBM: a row is read once into registers, reduced over the
-// threads that hold it, and written from the registers.  A thread holds V
-// vectors of 8 elements (16 bytes of bf16); rows of at most 1024 elements
-// take one warp each (no block barrier), longer rows one CTA each.
+// Both are bound by HBM.  Rows of at most 1024 elements take one warp each
+// (no block barrier), longer rows one CTA each; a thread has V vectors of 8
+// elements (16 bytes of bf16).  The forward reads a row into registers,
+// reduces it over the threads that hold it and writes from the registers;
+// several CTAs per SM hide each other's reduction.  The backward keeps its
+// CTAs for the whole call (their columns' sums of dw stay in registers) and
+// so has few of them: rows travel through a ring in shared memory, bulk
+// copies three to four stages ahead.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "quant_unit.cuh"
+#include "sm100.cuh"
 
 namespace fpq {
 
@@ -46,6 +51,16 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
                       f32x2_to_bf16x2(f[6], f[7]));
+}
+
+// Eight bf16 as four pairs of fp32 (paired fp32 instructions do two IEEE
+// operations each) and back.
+__device__ __forceinline__ void unpack4(const uint4& v, uint64_t (&p)[4]) {
+    p[0] = bf16x2_pair(v.x); p[1] = bf16x2_pair(v.y); p[2] = bf16x2_pair(v.z); p[3] = bf16x2_pair(v.w);
+}
+__device__ __forceinline__ uint4 pack4(const uint64_t (&p)[4]) {
+    return make_uint4(f32x2_to_bf16x2(lo_of(p[0]), hi_of(p[0])), f32x2_to_bf16x2(lo_of(p[1]), hi_of(p[1])),
+                      f32x2_to_bf16x2(lo_of(p[2]), hi_of(p[2])), f32x2_to_bf16x2(lo_of(p[3]), hi_of(p[3])));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -149,9 +164,11 @@ rmsnorm_quant_kernel(const NormArgs a) {
             const float sc = top ? __fdiv_rn(__uint_as_float(top), 448.0f) : 1.0f;
             uint32_t c[4];
             if (reciprocal_ok(sc)) {
-                const QuotientBracket b = quotient_bracket(sc);
+                // a quotient by the scale as a product with its reciprocal: 2^-23
+                // off at most, less than y itself
+                const float r = __frcp_rn(sc);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = e4m3x2_of_quotients(s[i][2 * j], s[i][2 * j + 1], b);
+                for (int j = 0; j < 4; ++j) c[j] = f32x2_to_e4m3x2(s[i][2 * j] * r, s[i][2 * j + 1] * r);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -202,109 +219,271 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
 // ------------------------------------------------------------------ backward
 
 struct NormBwdArgs {
-    const uint4* dy;
-    const uint4* x;        // row r at x + r ld
-    int64_t ld;            // in vectors of 8 elements
+    const uint8_t* dy;
+    const uint8_t* x;      // row r at x + r ld
+    int64_t ld;            // in bytes
     const uint4* w;
     const float* rstd;
-    const uint4* dres;     // or nullptr
+    const uint8_t* dres;   // or nullptr
     int64_t rows;
     int nvec;
     float cols;
     uint4* dx;
     float* partial;        // [grid, cols] sums of dw over a CTA's rows, or nullptr
+    int stages, batch;     // stages of a ring; rows per stage (1 for a CTA)
+    uint32_t* err;
 };
 
-// CTAs (or warps) take rows r, r + grid, ...; a thread's columns are the
-// same for every row, so dw stays in its registers until the end.
+constexpr int kBwdMaxStages = 4;
+constexpr int kBwdSmem = 216 * 1024;        // rings of the CTAs of an SM
+constexpr uint32_t kBwdWaitLimit = 1u << 16;         // polls that suspend the thread; well under a second
+
+// Global to shared memory, sizes and addresses multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar)) : "memory");
+}
+
+// A team (the CTA, or a warp) takes batches of consecutive rows, every
+// grid-th; a thread's columns are the same for every row.
 template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 512)
 rmsnorm_bwd_kernel(const NormBwdArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];         // w, then the rings: stages of dy, x, dres rows
+    __shared__ uint64_t bars[WARP ? kRowWarps : 1][kBwdMaxStages];
     __shared__ float red[2][32];
-    __shared__ __align__(16) float acc_s[WARP ? 1024 : 4];
-    pdl_trigger();
-    pdl_wait();
     const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, T = WARP ? 32 : blockDim.x;
-    const int64_t step = WARP ? (int64_t)gridDim.x * kRowWarps : gridDim.x;
-    uint4 wv[V];
-    float acc[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        wv[i] = t + i * T < a.nvec ? __ldg(a.w + t + i * T) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    const int team = WARP ? threadIdx.x >> 5 : 0;
+    const uint32_t row_bytes = (uint32_t)a.nvec * 16, part = row_bytes * a.batch;
+    uint4* const wsm = reinterpret_cast<uint4*>(smem);
+    uint8_t* const ring = smem + (row_bytes + 127) / 128 * 128 + team * a.stages * 3 * part;
+    uint64_t* const bar = bars[team];
+    pdl_trigger();
+    if (t == 0) {
+        for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
+        sm100::fence_barrier_init();
     }
-    int turn = 0;
-    for (int64_t row = WARP ? (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x; row < a.rows;
-         row += step, turn ^= 1) {
-        const int64_t dense = row * a.nvec;
-        const uint4* xr = a.x + row * a.ld;
-        uint4 dv[V], xv[V], ev[V];
+    pdl_wait();
+    for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) wsm[v] = __ldg(a.w + v);
+    __syncthreads();
+
+    const int64_t teams = WARP ? (int64_t)gridDim.x * kRowWarps : gridDim.x;
+    const int64_t first = WARP ? (int64_t)blockIdx.x * kRowWarps + team : blockIdx.x;
+    const int64_t batches = (a.rows + a.batch - 1) / a.batch;
+    const auto fill = [&](int64_t b, int stage) {            // one thread of the team
+        if (b >= batches) return;
+        const int64_t row = b * a.batch;
+        const uint32_t n = (uint32_t)min64(a.batch, a.rows - row), bytes = n * row_bytes;
+        uint8_t* dst = ring + stage * 3 * part;
+        sm100::mbar_arrive_expect_tx(&bar[stage], bytes * (a.dres ? 3 : 2));
+        bulk_load(dst, a.dy + row * row_bytes, bytes, &bar[stage]);
+        if (a.ld == row_bytes) {
+            bulk_load(dst + part, a.x + row * row_bytes, bytes, &bar[stage]);
+        } else {
+            for (uint32_t i = 0; i < n; ++i)
+                bulk_load(dst + part + i * row_bytes, a.x + (row + i) * a.ld, row_bytes, &bar[stage]);
+        }
+        if (a.dres) bulk_load(dst + 2 * part, a.dres + row * row_bytes, bytes, &bar[stage]);
+    };
+    if (t == 0)
+        for (int i = 0; i < a.stages; ++i) fill(first + i * teams, i);
+
+    // KEEP: the row stays in registers between the two passes, so that its
+    // stage is refilled between them; rows too long for that are read twice
+    constexpr bool KEEP = V <= 2;
+    uint64_t acc[V][4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = t + i * T;
-            dv[i] = xv[i] = ev[i] = make_uint4(0, 0, 0, 0);
-            if (v < a.nvec) {
-                dv[i] = ld_once(a.dy + dense + v);
-                xv[i] = ld_once(xr + v);
-                if (a.dres) ev[i] = ld_once(a.dres + dense + v);
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+    int turn = 0, stage = 0;
+    uint32_t phase = 0;
+    float next_rstd = first < batches ? __ldg(a.rstd + first * a.batch) : 0.0f;
+    for (int64_t b = first; b < batches; b += teams) {
+        if (!sm100::mbar_wait_bounded(&bar[stage], phase, kBwdWaitLimit)) {
+            raise_device_error(a.err, FPQ_ERR_DEVICE_TIMEOUT);
+            // the other copies in flight write to this CTA's shared memory
+            for (int i = 0; i < a.stages; ++i) sm100::mbar_wait_bounded(&bar[i], phase, kBwdWaitLimit);
+            return;
+        }
+        const int64_t row0 = b * a.batch;
+        const int n = (int)min64(a.batch, a.rows - row0);
+        for (int r = 0; r < n; ++r, turn ^= 1) {
+            const uint8_t* at = ring + stage * 3 * part + r * row_bytes;
+            const uint4* dv = reinterpret_cast<const uint4*>(at);
+            const uint4* xv = reinterpret_cast<const uint4*>(at + part);
+            const uint4* ev = reinterpret_cast<const uint4*>(at + 2 * part);
+            const float rstd = next_rstd;                    // loaded a row ahead
+            if (r + 1 < n) next_rstd = __ldg(a.rstd + row0 + r + 1);
+            else if (b + teams < batches) next_rstd = __ldg(a.rstd + (b + teams) * a.batch);
+            const uint64_t rstd2 = pack2(rstd, rstd);
+            uint64_t gw[KEEP ? V : 1][4], x[KEEP ? V : 1][4], dot2 = 0;   // dy w and x
+            uint4 e[KEEP ? V : 1];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = t + i * T, k = KEEP ? i : 0;
+                if (KEEP) e[k] = make_uint4(0, 0, 0, 0);
+                if (v >= a.nvec) continue;
+                uint64_t d[4], w[4];
+                unpack4(dv[v], d);
+                unpack4(xv[v], x[k]);
+                unpack4(wsm[v], w);
+                if (KEEP && a.dres) e[k] = ev[v];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    gw[k][j] = mul2(d[j], w[j]);
+                    dot2 = fma2(gw[k][j], x[k][j], dot2);
+                    acc[i][j] = fma2(d[j], mul2(x[k][j], rstd2), acc[i][j]);
+                }
+            }
+            const float dot = row_sum<WARP>(lo_of(dot2) + hi_of(dot2), red[turn]);
+            if (!WARP && t == 0) {
+                // every thread of the CTA is past its reads of this row (KEEP)
+                // or has left the previous one
+                if (KEEP) fill(b + a.stages * teams, stage);
+                else if (b != first) fill(b + (a.stages - 1) * teams, stage == 0 ? a.stages - 1 : stage - 1);
+            }
+            const float c = -__fdiv_rn(dot * rstd, a.cols) * rstd * rstd;
+            const uint64_t c2 = pack2(c, c);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = t + i * T, k = KEEP ? i : 0;
+                if (v >= a.nvec) continue;
+                if (!KEEP) {
+                    uint64_t d[4], w[4];
+                    unpack4(dv[v], d);
+                    unpack4(xv[v], x[k]);
+                    unpack4(wsm[v], w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) gw[k][j] = mul2(d[j], w[j]);
+                    e[k] = a.dres ? ev[v] : make_uint4(0, 0, 0, 0);
+                }
+                uint64_t out[4];
+                unpack4(e[k], out);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[j] = fma2(x[k][j], c2, fma2(gw[k][j], rstd2, out[j]));
+                st_v4(a.dx + (row0 + r) * a.nvec + v, pack4(out));
             }
         }
-        const float rstd = a.rstd[row];
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float d[8], x[8], w[8];
-            unpack8(dv[i], d);
-            unpack8(xv[i], x);
-            unpack8(wv[i], w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dot = fmaf(d[j] * w[j], x[j], dot);
-                acc[i][j] = fmaf(d[j], x[j] * rstd, acc[i][j]);
-            }
+        if (WARP) {
+            __syncwarp();
+            if (t == 0) fill(b + a.stages * teams, stage);
         }
-        dot = row_sum<WARP>(dot, red[turn]);
-        const float c = -__fdiv_rn(dot * rstd, a.cols) * rstd * rstd;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = t + i * T;
-            float d[8], x[8], w[8], e[8];
-            unpack8(dv[i], d);
-            unpack8(xv[i], x);
-            unpack8(wv[i], w);
-            unpack8(ev[i], e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] += fmaf(x[j], c, d[j] * w[j] * rstd);
-            if (v < a.nvec) st_v4(a.dx + dense + v, pack8(e));
-        }
+        if (++stage == a.stages) { stage = 0; phase ^= 1; }
     }
     if (!a.partial) return;
     float4* out = reinterpret_cast<float4*>(a.partial) + (int64_t)blockIdx.x * a.nvec * 2;
     if (WARP) {
-        // the CTA's eight warps add their sums in order
+        // the CTA's eight warps add their sums in order, in the rings' place
+        float* acc_s = reinterpret_cast<float*>(smem);
         for (int wi = 0; wi < kRowWarps; ++wi) {
-            if ((int)(threadIdx.x >> 5) == wi) {
+            __syncthreads();
+            if (team == wi) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (t + i * T < a.nvec)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float* p = &acc_s[(t + i * T) * 8 + j];
-                            *p = wi ? *p + acc[i][j] : acc[i][j];
+                            const float u = j & 1 ? hi_of(acc[i][j / 2]) : lo_of(acc[i][j / 2]);
+                            *p = wi ? *p + u : u;
                         }
             }
-            __syncthreads();
         }
+        __syncthreads();
         for (int v = threadIdx.x; v < 2 * a.nvec; v += blockDim.x) out[v] = reinterpret_cast<float4*>(acc_s)[v];
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = t + i * T;
             if (v < a.nvec) {
-                out[2 * v] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                out[2 * v + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+                out[2 * v] = make_float4(lo_of(acc[i][0]), hi_of(acc[i][0]), lo_of(acc[i][1]), hi_of(acc[i][1]));
+                out[2 * v + 1] = make_float4(lo_of(acc[i][2]), hi_of(acc[i][2]), lo_of(acc[i][3]), hi_of(acc[i][3]));
             }
+        }
+    }
+}
+
+// Rows of which no two fit in shared memory (more than 15360 elements): read
+// from global memory, four vectors at a time; with V = 8 a second time, from
+// L2, as the registers hold the sums of dw.
+template <int V>
+__global__ void __launch_bounds__(512)
+rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
+    __shared__ float red[2][32];
+    pdl_trigger();
+    pdl_wait();
+    const int t = threadIdx.x, T = blockDim.x;
+    uint64_t acc[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const uint4* dv = reinterpret_cast<const uint4*>(a.dy) + row * a.nvec;
+        const uint4* xv = reinterpret_cast<const uint4*>(a.x + row * a.ld);
+        const float rstd = __ldg(a.rstd + row);
+        const uint64_t rstd2 = pack2(rstd, rstd);
+        uint4 d[4], x[4];
+        const auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = t + (i0 + i) * T;
+                d[i] = x[i] = make_uint4(0, 0, 0, 0);
+                if (v < a.nvec) {
+                    d[i] = ld_once(dv + v);
+                    x[i] = ld_once(xv + v);
+                }
+            }
+        };
+        uint64_t dot2 = 0;
+#pragma unroll
+        for (int i0 = 0; i0 < V; i0 += 4) {
+            load(i0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = t + (i0 + i) * T;
+                uint64_t dp[4], xp[4], w[4];
+                unpack4(d[i], dp);
+                unpack4(x[i], xp);
+                unpack4(v < a.nvec ? __ldg(a.w + v) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dot2 = fma2(mul2(dp[j], w[j]), xp[j], dot2);
+                    acc[i0 + i][j] = fma2(dp[j], mul2(xp[j], rstd2), acc[i0 + i][j]);
+                }
+            }
+        }
+        const float dot = row_sum<false>(lo_of(dot2) + hi_of(dot2), red[turn]);
+        const float c = -__fdiv_rn(dot * rstd, a.cols) * rstd * rstd;
+        const uint64_t c2 = pack2(c, c);
+#pragma unroll
+        for (int i0 = 0; i0 < V; i0 += 4) {
+            if (V > 4) load(i0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = t + (i0 + i) * T;
+                if (v >= a.nvec) continue;
+                uint64_t dp[4], xp[4], w[4], out[4];
+                unpack4(d[i], dp);
+                unpack4(x[i], xp);
+                unpack4(__ldg(a.w + v), w);
+                unpack4(a.dres ? ld_once(reinterpret_cast<const uint4*>(a.dres) + row * a.nvec + v) : make_uint4(0, 0, 0, 0), out);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[j] = fma2(xp[j], c2, fma2(mul2(dp[j], w[j]), rstd2, out[j]));
+                st_v4(a.dx + row * a.nvec + v, pack4(out));
+            }
+        }
+    }
+    if (!a.partial) return;
+    float4* out = reinterpret_cast<float4*>(a.partial) + (int64_t)blockIdx.x * a.nvec * 2;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int v = t + i * T;
+        if (v < a.nvec) {
+            out[2 * v] = make_float4(lo_of(acc[i][0]), hi_of(acc[i][0]), lo_of(acc[i][1]), hi_of(acc[i][1]));
+            out[2 * v + 1] = make_float4(lo_of(acc[i][2]), hi_of(acc[i][2]), lo_of(acc[i][3]), hi_of(acc[i][3]));
         }
     }
 }
@@ -337,18 +516,47 @@ rmsnorm_dweight_kernel(const float4* __restrict__ partial, int parts, int nvec4,
     }
 }
 
-int bwd_vectors(int nvec) { return nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 2048 ? 4 : 8; }
+// How the backward of rows of nvec vectors is launched.
+struct BwdPlan {
+    int v, threads, ctas;      // vectors per thread, threads per CTA, CTAs per SM
+    int batch, stages, smem;   // rows per stage (warps), stages and bytes of shared memory per CTA
+};
 
-int bwd_threads(int nvec) {
-    if (nvec <= 128) return 32 * kRowWarps;
-    const int v = bwd_vectors(nvec);
-    return ((nvec + v - 1) / v + 31) / 32 * 32;
+// Longest row of the ring: w and two stages of three rows fit in kBwdSmem.
+constexpr int kRingVectors = kBwdSmem / 16 / 7 / 128 * 128;
+static_assert(kRingVectors * 16 + 2 * 3 * kRingVectors * 16 <= kBwdSmem, "a ring has two stages");
+
+BwdPlan bwd_plan(int nvec) {
+    BwdPlan p{};
+    const bool warp = nvec <= 128;
+    p.v = warp ? (nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4) : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
+    p.threads = warp ? 32 * kRowWarps : ((nvec + p.v - 1) / p.v + 31) / 32 * 32;
+    // short rows are copied several at a time, 2 KB per operand
+    p.batch = warp ? 128 / nvec : 1;
+    // About 512 threads per SM: with 8192 x 7168 (448 threads) one CTA of four
+    // stages takes 78 us and two of two stages 85 us, with 16384 x 2048 (128
+    // threads) two CTAs 74 us and four 65 us.
+    p.ctas = warp ? 1 : 512 / p.threads > 4 ? 4 : 512 / p.threads;
+    if (nvec > kRingVectors) return p;
+    const int row = nvec * 16, stage = 3 * row * p.batch * (warp ? kRowWarps : 1), w = (row + 127) / 128 * 128;
+    p.stages = (kBwdSmem / p.ctas - w) / stage;
+    if (p.stages > kBwdMaxStages) p.stages = kBwdMaxStages;
+    p.smem = w + p.stages * stage;
+    if (warp && p.smem < nvec * 32) p.smem = nvec * 32;      // the warps' sums
+    return p;
 }
 
-// About 1024 threads per SM: the registers of more do not fit.
-int bwd_grid(int64_t rows, int nvec, int sms) {
-    const int64_t tasks = nvec <= 128 ? (rows + kRowWarps - 1) / kRowWarps : rows;
-    return (int)min64(tasks, (int64_t)sms * (nvec <= 128 ? 4 : max64(1, 1024 / bwd_threads(nvec))));
+int bwd_grid(int64_t rows, const BwdPlan& p, int nvec, int sms) {
+    const int64_t tasks = nvec <= 128 ? ((rows + p.batch - 1) / p.batch + kRowWarps - 1) / kRowWarps : rows;
+    return (int)min64(tasks, (int64_t)sms * p.ctas);
+}
+
+template <int V, bool WARP>
+cudaError_t launch_bwd(const NormBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t st) {
+    const auto kernel = rmsnorm_bwd_kernel<V, WARP>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3((unsigned)p.threads), p.smem, st, a);
 }
 
 }  // namespace
@@ -363,23 +571,29 @@ cudaError_t launch_rmsnorm_quantize(int fmt, const void* x, int64_t ld_x, const 
 }
 
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, int sms) {
-    return (size_t)bwd_grid(rows, (int)(cols / 8), sms) * (size_t)cols * sizeof(float);
+    const int nvec = (int)(cols / 8);
+    return (size_t)bwd_grid(rows, bwd_plan(nvec), nvec, sms) * (size_t)cols * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight,
                                     const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
-                                    float* dweight, void* workspace, int sms, cudaStream_t st) {
-    const int nvec = (int)(cols / 8), grid = bwd_grid(rows, nvec, sms);
-    const NormBwdArgs a{(const uint4*)dy, (const uint4*)x, ld_x / 8, (const uint4*)weight, rstd, (const uint4*)dres,
-                        rows, nvec, (float)cols, (uint4*)dx, dweight ? (float*)workspace : nullptr};
+                                    float* dweight, void* workspace, uint32_t* err, int sms, cudaStream_t st) {
+    const int nvec = (int)(cols / 8);
+    const BwdPlan p = bwd_plan(nvec);
+    const int grid = bwd_grid(rows, p, nvec, sms);
+    const NormBwdArgs a{(const uint8_t*)dy, (const uint8_t*)x, ld_x * 2, (const uint4*)weight, rstd,
+                        (const uint8_t*)dres, rows, nvec, (float)cols, (uint4*)dx,
+                        dweight ? (float*)workspace : nullptr, p.stages, p.batch, err};
     cudaError_t e = cudaSuccess;
     if (grid > 0) {
-        const dim3 g((unsigned)grid), b((unsigned)bwd_threads(nvec));
-        if (nvec <= 32) e = launch_pdl(rmsnorm_bwd_kernel<1, true>, g, b, 0, st, a);
-        else if (nvec <= 64) e = launch_pdl(rmsnorm_bwd_kernel<2, true>, g, b, 0, st, a);
-        else if (nvec <= 128) e = launch_pdl(rmsnorm_bwd_kernel<4, true>, g, b, 0, st, a);
-        else if (nvec <= 2048) e = launch_pdl(rmsnorm_bwd_kernel<4, false>, g, b, 0, st, a);
-        else e = launch_pdl(rmsnorm_bwd_kernel<8, false>, g, b, 0, st, a);
+        const dim3 g((unsigned)grid), b((unsigned)p.threads);
+        if (nvec <= 32) e = launch_bwd<1, true>(a, p, grid, st);
+        else if (nvec <= 64) e = launch_bwd<2, true>(a, p, grid, st);
+        else if (nvec <= 128) e = launch_bwd<4, true>(a, p, grid, st);
+        else if (nvec <= 1024) e = launch_bwd<2, false>(a, p, grid, st);
+        else if (nvec <= kRingVectors) e = launch_bwd<4, false>(a, p, grid, st);
+        else if (nvec <= 2048) e = launch_pdl(rmsnorm_bwd_long_kernel<4>, g, b, 0, st, a);
+        else e = launch_pdl(rmsnorm_bwd_long_kernel<8>, g, b, 0, st, a);
     }
     if (e != cudaSuccess || !dweight) return e;
     return launch_pdl(rmsnorm_dweight_kernel, dim3((unsigned)((2 * nvec + 31) / 32)), dim3(1024), 0, st,

@@ -32,7 +32,8 @@ def _inside(got, want, size, adds, dtype):
 
 
 @pytest.mark.parametrize("tokens,topk,hidden", [(1, 1, 8), (1, 8, 7168), (5, 3, 40), (33, 8, 2048), (7, 9, 2056),
-                                                (3, 32, 264), (200, 2, 136), (2, 4, 16392)])
+                                                (3, 32, 264), (200, 2, 136), (2, 4, 16392),
+                                                (2400, 2, 72), (2401, 3, 552), (2500, 11, 136)])
 @pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_forward_and_backward(fpq, tokens, topk, hidden, y_dtype, out_dtype):

@@ -167,12 +167,14 @@ def _ref_backward(dy, x, w, rstd, dres):
     return dx, size, (d * v * r).sum(0), (d * v * r).abs().sum(0)
 
 
-@pytest.mark.parametrize("rows,cols", SHAPES + [(1, 8), (4, 40), (2050, 64), (1500, 1032), (40, 16392)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(1, 8), (4, 40), (2050, 64), (1500, 1032), (40, 16392),
+                                                (1500, 2048), (900, 4096), (310, 16384), (310, 16392)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_backward(fpq, rows, cols, residual):
     """Errors count against the sums of magnitudes: 2^-17 of them covers the
     dot product's additions (at most 74) and, for dweight, those over rows (a
-    CTA's rows, then its share of the partial rows: under 100)."""
+    CTA's rows, then its share of the partial rows: under 100; each at most
+    2^-24 of the sum)."""
     x, w, _ = _data(rows, cols, rows + cols + 1)
     g = torch.Generator().manual_seed(3)
     dy = torch.randn((rows, cols), generator=g).to(BF16).cuda()
