@@ -770,7 +770,7 @@ fpq_status fpq_gemv_nvfp4(const void* x, int64_t m, const void* wq, const void* 
     if ((st = check_ptrs({x, wq, ws, y})) != FPQ_OK) return st;
     const DeviceState* d = device_state(&st);
     if (!d) return st;
-    return from_cuda(fpq::launch_gemv_nvfp4(x, m, 1, nullptr, 1, wq, ws, wg, n, k, y, y_dtype == FPQ_OUT_F32, d->err,
+    return from_cuda(fpq::launch_gemv_nvfp4(x, m, 1, (int)m, nullptr, 1, wq, ws, wg, n, k, y, y_dtype == FPQ_OUT_F32, d->err,
                                             d->sms, (cudaStream_t)stream),
                      "nvfp4 gemv launch");
 }
@@ -791,7 +791,7 @@ fpq_status fpq_moe_gemv_nvfp4(const void* x, int32_t x_per_pair, const int32_t* 
     if ((st = check_ptrs({x, ids, wq, ws, y})) != FPQ_OK) return st;
     const DeviceState* d = device_state(&st);
     if (!d) return st;
-    return from_cuda(fpq::launch_gemv_nvfp4(x, tokens * topk, x_per_pair ? 1 : topk, ids, num_experts, wq, ws, wg, n,
+    return from_cuda(fpq::launch_gemv_nvfp4(x, tokens * topk, x_per_pair ? 1 : topk, (int)tokens, ids, num_experts, wq, ws, wg, n,
                                             k, y, y_dtype == FPQ_OUT_F32, d->err, d->sms, (cudaStream_t)stream),
                      "nvfp4 expert gemv launch");
 }

@@ -43,10 +43,10 @@ namespace fpq {
 
 namespace {
 
-constexpr int kGemvWarps = 8;
+constexpr int kGemvWarps = 16;             // of an SM, in one CTA or two
 constexpr int kBlock = 128;               // weights of a row per warp and step
 constexpr int kGroup = 4;                 // blocks per group
-constexpr int kXBytes = 56 * 1024;        // shared memory for x, unless one group per warp needs more
+constexpr int kXBytes = 112 * 1024;       // of an SM for x, unless a CTA's warps need more for a group each
 
 struct GemvArgs {
     const uint16_t* x;          // row m at x + (m / x_div) k
@@ -61,6 +61,7 @@ struct GemvArgs {
     void* y;                    // [m, n]
     uint32_t* err;
     int y_f32;
+    int cap;                    // pairs of an expert that a CTA takes (at most the columns)
     int wk, wr;                 // warps along k, row tiles per CTA
     int chunk;                  // groups of x in shared memory at a time, a multiple of wk
 };
@@ -121,13 +122,13 @@ struct Block {                             // a lane's 32 codes and two scales o
     uint32_t s[2];
 };
 
-// TILES: column tiles of eight (rows of x).
-template <int TILES>
-__global__ void __launch_bounds__(32 * kGemvWarps, 2)
+// TILES: column tiles of eight (rows of x); CTAS: CTAs per SM.
+template <int TILES, int CTAS>
+__global__ void __launch_bounds__(32 * kGemvWarps / CTAS, CTAS)
 gemv_nvfp4_kernel(const GemvArgs a) {
     constexpr int COLS = 8 * TILES;
     extern __shared__ __align__(16) uint8_t smem[];         // per column: a chunk of x, then its blocks' factors
-    __shared__ float red[kGemvWarps][32][COLS / 2];
+    __shared__ float red[kGemvWarps / CTAS][32][COLS / 2];
     __shared__ int member[COLS], xrow[COLS], info[2];       // info: members, occurrences before this pair
     pdl_trigger();
     pdl_wait();
@@ -137,8 +138,8 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     int64_t e = 0;
     int count;
     if (a.ids) {
-        // blockIdx.y is a pair; every COLS-th pair of an expert takes itself
-        // and the next COLS - 1, the others have nothing to do
+        // blockIdx.y is a pair; every cap-th pair of an expert takes itself and
+        // the next cap - 1, the others have nothing to do
         const int p = blockIdx.y, id = a.ids[p];
         e = id;
         if (id < 0 || id >= a.experts) {
@@ -151,17 +152,17 @@ gemv_nvfp4_kernel(const GemvArgs a) {
         // later ones (one warp does both if it is alone)
         if (warp == threads / 32 - 1) {
             int found = 0;
-            for (int q = p; q < a.m && found < COLS; q += 32) {
+            for (int q = p; q < a.m && found < a.cap; q += 32) {
                 const bool same = q + lane < a.m && a.ids[q + lane] == id;
                 const uint32_t mask = __ballot_sync(0xFFFFFFFFu, same);
                 const int at = found + __popc(mask & ((1u << lane) - 1u));
-                if (same && at < COLS) {
+                if (same && at < a.cap) {
                     member[at] = q + lane;
                     xrow[at] = (q + lane) / a.x_div;
                 }
                 found += __popc(mask);
             }
-            if (lane == 0) info[0] = min(found, COLS);
+            if (lane == 0) info[0] = min(found, a.cap);
         }
         if (warp == 0) {
             int before = 0;
@@ -170,7 +171,7 @@ gemv_nvfp4_kernel(const GemvArgs a) {
             if (lane == 0) info[1] = before;
         }
         __syncthreads();
-        if (info[1] % COLS) return;
+        if (info[1] % a.cap) return;
         count = info[0];
     } else {
         count = a.m;
@@ -207,14 +208,16 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     // eight columns of a read fall on different banks.
     const int chunk_blocks = a.chunk * kGroup;
     const int x_stride = chunk_blocks * 256 + (chunk_blocks * 4 + 127) / 128 * 128 + 64;
+    // A unit is 64 bytes, the 32 elements of a lane's block; four adjacent
+    // threads hold a block.
+    const int col_units = chunk_blocks * 4, step_col = threads / col_units, step_u = threads % col_units;
     const auto stage = [&](int group0) {
-        // four adjacent threads hold a block: 32 elements each
-        const int units = count * chunk_blocks * 4;
-        for (int i0 = 0; i0 < units; i0 += threads) {
-            const int i = i0 + tid, col = i / (chunk_blocks * 4), u = i - col * (chunk_blocks * 4);
+        int col = tid / col_units, u = tid % col_units;
+        for (int i = warp * 32; i < count * col_units; i += threads) {      // whole warps: there are shuffles
             const int k0 = group0 * (kGroup * kBlock) + u * 32;
+            const bool in = col < count;
             uint4 v[4] = {};
-            if (i < units && k0 < a.k) {
+            if (in && k0 < a.k) {
                 const uint4* src = reinterpret_cast<const uint4*>(a.x + (int64_t)xrow[col] * a.k + k0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = __ldg(src + j);
@@ -229,8 +232,9 @@ gemv_nvfp4_kernel(const GemvArgs a) {
             // or a NaN (the finite elements stay finite), 0 for a zero block
             const int f = top >= 0x7F80u ? -112 : top == 0 ? 0 : min(127, 141 - (int)(top >> 7));
             const uint32_t s1 = (uint32_t)(127 + f) << 7, s2 = s1 | (s1 << 16);
-            if (i < units) {
-                uint8_t* dst = smem + col * x_stride + (u >> 2) * 256 + (u & 3) * 16;
+            if (in) {
+                uint8_t* const column = smem + col * x_stride;
+                uint8_t* const dst = column + (u >> 2) * 256 + (u & 3) * 16;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -241,9 +245,11 @@ gemv_nvfp4_kernel(const GemvArgs a) {
                     }
                     *reinterpret_cast<uint4*>(dst + 64 * j) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if ((u & 3) == 0)
-                    reinterpret_cast<float*>(smem + col * x_stride + chunk_blocks * 256)[u >> 2] = pow2_neg(f);
+                if ((u & 3) == 0) reinterpret_cast<float*>(column + chunk_blocks * 256)[u >> 2] = pow2_neg(f);
             }
+            col += step_col;
+            u += step_u;
+            if (u >= col_units) { u -= col_units; ++col; }
         }
     };
 
@@ -323,14 +329,14 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     }
 }
 
-template <int TILES>
+template <int TILES, int CTAS>
 cudaError_t gemv(GemvArgs a, cudaStream_t st) {
-    const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock), cols = a.m < 8 * TILES ? a.m : 8 * TILES;
-    const int fit = kXBytes / (cols * kGroup * 256) / a.wk * a.wk, all = (groups + a.wk - 1) / a.wk * a.wk;
+    const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock), cols = a.ids ? a.cap : a.m;
+    const int fit = kXBytes / CTAS / (cols * kGroup * 256) / a.wk * a.wk, all = (groups + a.wk - 1) / a.wk * a.wk;
     a.chunk = fit < a.wk ? a.wk : fit < all ? fit : all;
     const int blocks = a.chunk * kGroup;
     const int smem = cols * (blocks * 256 + (blocks * 4 + 127) / 128 * 128 + 64);
-    const auto kernel = gemv_nvfp4_kernel<TILES>;
+    const auto kernel = gemv_nvfp4_kernel<TILES, CTAS>;
     if (smem > 32 * 1024) {                                  // with the static arrays, past what needs no opt-in
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -342,23 +348,30 @@ cudaError_t gemv(GemvArgs a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, const int32_t* ids, int experts, const void* wq,
-                              const void* ws, const float* wg, int64_t n, int64_t k, void* y, int y_f32,
-                              uint32_t* err, int sms, cudaStream_t st) {
-    // An SM holds two CTAs, sixteen warps.  As many warps along k as leave one
-    // wave (and a group per warp), then as many row tiles per CTA as bring the
-    // CTAs into one wave: with 148 SMs, 2048 tiles become 293 CTAs of seven
-    // warps, 128 tiles 128 CTAs of eight.  The expert form counts on eight
-    // experts per call.
+cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, const int32_t* ids, int experts,
+                              const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
+                              int y_f32, uint32_t* err, int sms, cudaStream_t st) {
+    // As many warps along k as leave one wave of an SM's sixteen (and a group
+    // per warp; at most eight), then as many row tiles per CTA as bring the
+    // CTAs into one wave: with 148 SMs and two CTAs each, 2048 tiles become
+    // 293 CTAs of seven warps, 128 tiles 128 CTAs of eight.  The expert form
+    // counts on eight experts per call.
     const int64_t tiles = (n + 15) / 16, waves = tiles * (ids ? 8 : 1), groups = (k + kGroup * kBlock - 1) / (kGroup * kBlock);
-    int wk = kGemvWarps;
-    while (wk > 1 && (waves * wk > 2 * kGemvWarps * (int64_t)sms || groups < wk)) wk /= 2;
-    const int64_t wr = max64(1, min64(kGemvWarps / wk, (waves + 2 * sms - 1) / (2 * sms)));
-    const GemvArgs a{(const uint16_t*)x, (int)m, x_div, ids, experts, (const uint8_t*)wq, (const uint8_t*)ws, wg, n,
-                     (int)k, y, err, y_f32, wk, (int)wr, 0};
-    // Sixteen columns where an expert can be expected to have more than eight pairs.
+    int wk = 8;
+    while (wk > 1 && (waves * wk > kGemvWarps * (int64_t)sms || groups < wk)) wk /= 2;
+    // Sixteen columns for more than eight rows, or where an expert can be
+    // expected to have more than eight pairs.  Then one CTA per SM: x fills
+    // its shared memory, and is converted once for twice the weights.
     const bool wide = ids ? m > 8 && m > 4 * (int64_t)experts : m > 8;
-    return wide ? gemv<2>(a, st) : gemv<1>(a, st);
+    const int ctas = wide ? 1 : 2;
+    const int64_t wr = max64(1, min64(kGemvWarps / ctas / wk, (waves + ctas * sms - 1) / (ctas * sms)));
+    // An expert has at most a pair of each token (of a token that names it
+    // twice, two).  Four where that is far above the average: they take half
+    // of the shared memory of eight, which is the loads' cache.
+    const int cap = wide ? 16 : tokens < 4 ? tokens : m <= 2 * (int64_t)experts ? 4 : 8;
+    const GemvArgs a{(const uint16_t*)x, (int)m, x_div, ids, experts, (const uint8_t*)wq, (const uint8_t*)ws, wg, n,
+                     (int)k, y, err, y_f32, cap, wk, (int)wr, 0};
+    return wide ? gemv<2, 1>(a, st) : gemv<1, 2>(a, st);
 }
 
 }  // namespace fpq

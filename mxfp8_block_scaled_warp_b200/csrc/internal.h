@@ -140,9 +140,9 @@ cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const vo
 
 // Few rows times NVFP4 weights (gemv_nvfp4.cu): row m of y [m, n] is row
 // m / x_div of x times the matrix (ids == nullptr) or expert ids[m]'s.
-cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, const int32_t* ids, int experts, const void* wq,
-                              const void* ws, const float* wg, int64_t n, int64_t k, void* y, int y_f32,
-                              uint32_t* err, int sms, cudaStream_t st);
+cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, const int32_t* ids, int experts,
+                              const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
+                              int y_f32, uint32_t* err, int sms, cudaStream_t st);
 
 // Set the per-thread detail string returned by fpq_last_error_detail().
 void set_error_detail(const char* what);

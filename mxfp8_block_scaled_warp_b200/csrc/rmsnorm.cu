@@ -236,13 +236,6 @@ struct NormBwdArgs {
 
 constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 216 * 1024;        // rings of the CTAs of an SM
-constexpr uint32_t kBwdWaitLimit = 1u << 16;         // polls that suspend the thread; well under a second
-
-// Global to shared memory, sizes and addresses multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar)) : "memory");
-}
 
 // A team (the CTA, or a warp) takes batches of consecutive rows, every
 // grid-th; a thread's columns are the same for every row.
@@ -276,14 +269,14 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
         const uint32_t n = (uint32_t)min64(a.batch, a.rows - row), bytes = n * row_bytes;
         uint8_t* dst = ring + stage * 3 * part;
         sm100::mbar_arrive_expect_tx(&bar[stage], bytes * (a.dres ? 3 : 2));
-        bulk_load(dst, a.dy + row * row_bytes, bytes, &bar[stage]);
+        sm100::bulk_load(dst, a.dy + row * row_bytes, bytes, &bar[stage]);
         if (a.ld == row_bytes) {
-            bulk_load(dst + part, a.x + row * row_bytes, bytes, &bar[stage]);
+            sm100::bulk_load(dst + part, a.x + row * row_bytes, bytes, &bar[stage]);
         } else {
             for (uint32_t i = 0; i < n; ++i)
-                bulk_load(dst + part + i * row_bytes, a.x + (row + i) * a.ld, row_bytes, &bar[stage]);
+                sm100::bulk_load(dst + part + i * row_bytes, a.x + (row + i) * a.ld, row_bytes, &bar[stage]);
         }
-        if (a.dres) bulk_load(dst + 2 * part, a.dres + row * row_bytes, bytes, &bar[stage]);
+        if (a.dres) sm100::bulk_load(dst + 2 * part, a.dres + row * row_bytes, bytes, &bar[stage]);
     };
     if (t == 0)
         for (int i = 0; i < a.stages; ++i) fill(first + i * teams, i);
@@ -300,10 +293,8 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     uint32_t phase = 0;
     float next_rstd = first < batches ? __ldg(a.rstd + first * a.batch) : 0.0f;
     for (int64_t b = first; b < batches; b += teams) {
-        if (!sm100::mbar_wait_bounded(&bar[stage], phase, kBwdWaitLimit)) {
+        if (!sm100::mbar_wait_seconds(&bar[stage], phase)) {     // after this long no copy is in flight
             raise_device_error(a.err, FPQ_ERR_DEVICE_TIMEOUT);
-            // the other copies in flight write to this CTA's shared memory
-            for (int i = 0; i < a.stages; ++i) sm100::mbar_wait_bounded(&bar[i], phase, kBwdWaitLimit);
             return;
         }
         const int64_t row0 = b * a.batch;
