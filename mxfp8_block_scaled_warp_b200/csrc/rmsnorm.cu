@@ -44,15 +44,6 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
-                      f32x2_to_bf16x2(f[6], f[7]));
-}
-
 // Eight bf16 as four pairs of fp32 (paired fp32 instructions do two IEEE
 // operations each) and back.
 __device__ __forceinline__ void unpack4(const uint4& v, uint64_t (&p)[4]) {
@@ -61,6 +52,18 @@ __device__ __forceinline__ void unpack4(const uint4& v, uint64_t (&p)[4]) {
 __device__ __forceinline__ uint4 pack4(const uint64_t (&p)[4]) {
     return make_uint4(f32x2_to_bf16x2(lo_of(p[0]), hi_of(p[0])), f32x2_to_bf16x2(lo_of(p[1]), hi_of(p[1])),
                       f32x2_to_bf16x2(lo_of(p[2]), hi_of(p[2])), f32x2_to_bf16x2(lo_of(p[3]), hi_of(p[3])));
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The larger magnitude with the product of the signs, NaN if either is NaN.
+__device__ __forceinline__ float absmax_f32(float a, float b) {
+    float d;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -127,65 +130,69 @@ rmsnorm_quant_kernel(const NormArgs a) {
             if (a.res) rv[i] = ld_once(a.res + dense + v);
         }
     }
-    float s[V][8], sq = 0.0f;
+    uint64_t s[V][4], sq2 = 0;                              // pairs
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float r[8];
-        unpack8(xv[i], s[i]);
+        unpack4(xv[i], s[i]);
         if (a.res) {
-            unpack8(rv[i], r);
+            uint64_t r[4];
+            unpack4(rv[i], r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+            for (int j = 0; j < 4; ++j) s[i][j] = add2(s[i][j], r[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+        for (int j = 0; j < 4; ++j) sq2 = fma2(s[i][j], s[i][j], sq2);
         const int v = t + i * T;
-        if (a.h && v < a.nvec) st_v4(a.h + dense + v, pack8(s[i]));
+        if (a.h && v < a.nvec) st_v4(a.h + dense + v, pack4(s[i]));
     }
-    sq = row_sum<WARP>(sq, red);
+    const float sq = row_sum<WARP>(lo_of(sq2) + hi_of(sq2), red);
     const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(sq, a.cols) + a.eps));
     if (a.rstd && t == 0) a.rstd[row] = rstd;
+    const uint64_t rstd2 = pack2(rstd, rstd);
 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = t + i * T;
         const bool in = v < a.nvec;
-        float w[8];
-        unpack8(in ? __ldg(a.w + v) : make_uint4(0, 0, 0, 0), w);
-        uint32_t top = 0;
+        uint64_t w[4];
+        unpack4(in ? __ldg(a.w + v) : make_uint4(0, 0, 0, 0), w);
+        float most = 0.0f;                                   // largest magnitude, but for its sign; NaN if there is one
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s[i][j] = s[i][j] * rstd * w[j];
-            top = max(top, __float_as_uint(s[i][j]) & 0x7FFFFFFFu);   // NaN patterns order above infinity
+        for (int j = 0; j < 4; ++j) {
+            s[i][j] = mul2(mul2(s[i][j], rstd2), w[j]);
+            most = absmax_f32(most, absmax_f32(lo_of(s[i][j]), hi_of(s[i][j])));
         }
-        if (a.y && in) st_v4(a.y + dense + v, pack8(s[i]));
+        uint32_t top = __float_as_uint(most) & 0x7FFFFFFFu;  // NaN patterns order above infinity
+        if (a.y && in) st_v4(a.y + dense + v, pack4(s[i]));
         if (FMT == kNormFp8) {
             top = group_max<16>(in ? top : 0u);             // the 16 lanes of a 128-element tile, in or out together
             const float sc = top ? __fdiv_rn(__uint_as_float(top), 448.0f) : 1.0f;
-            uint32_t c[4];
+            uint32_t c[2];
             if (reciprocal_ok(sc)) {
                 // a quotient by the scale as a product with its reciprocal: 2^-23
                 // off at most, less than y itself
                 const float r = __frcp_rn(sc);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = f32x2_to_e4m3x2(s[i][2 * j] * r, s[i][2 * j + 1] * r);
+                const uint64_t r2 = pack2(r, r);
+                c[0] = e4m3x4_of_pairs(mul2(s[i][0], r2), mul2(s[i][1], r2));
+                c[1] = e4m3x4_of_pairs(mul2(s[i][2], r2), mul2(s[i][3], r2));
             } else {
+                uint64_t d[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c[j] = f32x2_to_e4m3x2(__fdiv_rn(s[i][2 * j], sc), __fdiv_rn(s[i][2 * j + 1], sc));
+                for (int j = 0; j < 4; ++j) d[j] = pack2(__fdiv_rn(lo_of(s[i][j]), sc), __fdiv_rn(hi_of(s[i][j]), sc));
+                c[0] = e4m3x4_of_pairs(d[0], d[1]);
+                c[1] = e4m3x4_of_pairs(d[2], d[3]);
             }
             if (in) {
-                st_v2(a.q + dense + v, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)));
+                st_v2(a.q + dense + v, make_uint2(c[0], c[1]));
                 if ((v & 15) == 0) static_cast<float*>(a.scales)[(dense + v) >> 4] = sc;
             }
         } else if (FMT == kNormMx) {
             top = group_max<4>(in ? top : 0u);
             const int e = mx_exponent_f32(top);
             const float mul = pow2_neg(e == 128 ? 127 : e);
-            uint32_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = f32x2_to_e4m3x2(s[i][2 * j] * mul, s[i][2 * j + 1] * mul);
-            uint2 q = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+            const uint64_t mul_2 = pack2(mul, mul);
+            uint2 q = make_uint2(e4m3x4_of_pairs(mul2(s[i][0], mul_2), mul2(s[i][1], mul_2)),
+                                 e4m3x4_of_pairs(mul2(s[i][2], mul_2), mul2(s[i][3], mul_2)));
             if (e == 128) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
             if (in) {
                 st_v2(a.q + dense + v, q);
