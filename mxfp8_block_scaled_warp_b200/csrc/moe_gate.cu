@@ -369,7 +369,7 @@ moe_gate_kernel(const GateArgs a) {
 // their lists: the larger of element i of one and 7 - i of the other are the
 // eight largest of both, in bitonic order.  No step waits for the one before
 // as in taking maxima one after the other, and the four tokens of a warp
-// share the instructions: 40 per token for 64 bf16 logits.  A key carries its
+// share the instructions: 110 per token for 64 bf16 logits.  A key carries its
 // index, so that equal logits compare by it: in the lower half of a bf16
 // logit's pattern (which is the type's own width), else in a second word.
 template <int LANES, typename T> struct MergeKey;
@@ -492,11 +492,85 @@ struct GateBwdArgs {
 //   softmax, renormalize: dl_j = c_j (v_j - sum_i v_i c_i), 0 where not
 //     chosen, c = softmax over the chosen logits
 //   softmax:              dl_e = p_e (ds_e - sum_i v_i p_i), ds_e = v_j at id j
-// Only the last one reads every logit; the others read the chosen ones.  The
-// row is assembled in shared memory and written with 16-byte stores.
-template <typename T, bool SIGMOID>
+// Only the last one reads every logit.
+__device__ __forceinline__ int checked_id(const GateBwdArgs& a, int64_t tok, int choice, bool in) {
+    if (!in) return -1;
+    const int id = a.ids[tok * a.topk + choice];
+    if (id >= 0 && id < a.experts) return id;
+    raise_device_error(a.err, FPQ_ERR_DEVICE_BAD_INPUT);     // its gradient is dropped
+    return -1;
+}
+
+// The first three: LANES lanes per token (at least topk), choice j in lane j.
+// They write zeros, 16 bytes at a time, and then the few values.
+template <typename T, bool SIGMOID, int LANES>
 __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_bwd_kernel(const GateBwdArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, s = lane % LANES, E = a.experts;
+    const int64_t tok = ((int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * (32 / LANES) + lane / LANES;
+    const bool live = tok < a.tokens;                        // the warp's other tokens go on
+    const int id = checked_id(a, tok, s, live && s < a.topk);
+    const bool have = id >= 0;
+    const float x = have ? load_logit<T>(static_cast<const T*>(a.logits) + tok * E + id) : -INFINITY;
+    const float v = have ? a.scale * a.dweights[tok * a.topk + s] : 0.0f;
+    T* out = static_cast<T*>(a.dlogits) + tok * E;
+    const auto put = [&](int e, float f) {
+        if (sizeof(T) == 4) reinterpret_cast<float*>(out)[e] = f;
+        else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(f);
+    };
+    if (live) {
+        constexpr int per = 16 / (int)sizeof(T);
+        if (E % per == 0) {
+            for (int i = s; i < E / per; i += LANES) st_v4(reinterpret_cast<uint4*>(out) + i, make_uint4(0, 0, 0, 0));
+        } else {
+            for (int e = s; e < E; e += LANES) put(e, 0.0f);
+        }
+    }
+    const auto token_sum = [&](float f) {
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) f += __shfl_xor_sync(kFull, f, o);
+        return f;
+    };
+    float g;                                                 // what the choice adds at its id
+    if (SIGMOID) {
+        const float p = have ? sigmoid(x) : 0.0f, q = have ? sigmoid(-x) : 0.0f;   // q = 1 - p without cancellation
+        g = v;
+        if (a.renormalize) {
+            const float P = token_sum(p), vp = token_sum(v * p);
+            g = P == 0.0f ? 0.0f : __fdiv_rn(v - __fdiv_rn(vp, P), P);
+        }
+        g = g * p * q;
+    } else {
+        float mx = x;
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        const float c = have && mx != -INFINITY ? expf(x - mx) : 0.0f;
+        const float total = token_sum(c), vc = token_sum(v * c);
+        g = total == 0.0f ? 0.0f : __fdiv_rn(c, total) * (v - __fdiv_rn(vc, total));
+    }
+    // an id named twice gets the sum, in the order of the choices, with its
+    // first choice
+    const uint32_t same = __match_any_sync(kFull, have ? id | (lane / LANES) << 16 : -1 - lane);
+    const bool first = have && __ffs(same) - 1 == lane;
+    if (__any_sync(kFull, have && !first)) {
+        float total = 0.0f;
+        for (int j = 0; j < 32; ++j) {
+            const float gj = __shfl_sync(kFull, g, j);
+            if ((same >> j) & 1u) total += gj;
+        }
+        g = total;
+    }
+    __syncwarp();                                            // after the zeros
+    if (first) put(id, g);
+}
+
+// The softmax over all experts: a warp per token, its row assembled in shared
+// memory.
+template <typename T>
+__global__ void __launch_bounds__(32 * kGateWarps)
+moe_gate_bwd_dense_kernel(const GateBwdArgs a) {
     extern __shared__ __align__(16) float sh[];
     pdl_trigger();
     pdl_wait();
@@ -505,77 +579,36 @@ moe_gate_bwd_kernel(const GateBwdArgs a) {
     if (tok >= a.tokens) return;
     float* d = sh + warp * ((E + 3) / 4 * 4);
     const T* row = static_cast<const T*>(a.logits) + tok * E;
-
-    int id = lane < K ? a.ids[tok * K + lane] : -1;
-    if (lane < K && (id < 0 || id >= E)) {
-        raise_device_error(a.err, FPQ_ERR_DEVICE_BAD_INPUT);
-        id = -1;                                             // its gradient is dropped
-    }
+    const int id = checked_id(a, tok, lane, lane < K);
     const bool have = id >= 0;
     const float v = have ? a.scale * a.dweights[tok * K + lane] : 0.0f;
     const float x = have ? load_logit<T>(row + id) : -INFINITY;
-    for (int e = lane; e < E; e += 32) d[e] = 0.0f;
-    __syncwarp();
-
-    float g = 0.0f;                                          // what choice `lane` adds at its id
-    float mx = -INFINITY, sum = 0.0f, dot = 0.0f;
-    if (SIGMOID) {
-        const float p = have ? sigmoid(x) : 0.0f, q = have ? sigmoid(-x) : 0.0f;   // q = 1 - p without cancellation
-        g = v;
-        if (a.renormalize) {
-            const float P = warp_sum(p);
-            const float mean = P == 0.0f ? 0.0f : __fdiv_rn(warp_sum(v * p), P);
-            g = P == 0.0f ? 0.0f : __fdiv_rn(v - mean, P);
-        }
-        g = g * p * q;
-    } else if (a.renormalize) {
-        mx = warp_max(x);
-        const float c = have && mx != -INFINITY ? expf(x - mx) : 0.0f;
-        const float total = warp_sum(c), vc = warp_sum(v * c);
-        g = total == 0.0f ? 0.0f : __fdiv_rn(c, total) * (v - __fdiv_rn(vc, total));
-    } else {
-        for (int e = lane; e < E; e += 32) mx = fmaxf(mx, load_logit<T>(row + e));
-        mx = warp_max(mx);
-        if (mx != -INFINITY) {
-            for (int e = lane; e < E; e += 32) sum += expf(load_logit<T>(row + e) - mx);
-            sum = warp_sum(sum);
-        }
-        const float p = have && mx != -INFINITY ? __fdiv_rn(expf(x - mx), sum) : 0.0f;
-        dot = warp_sum(v * p);
-        g = v;
+    float mx = -INFINITY, sum = 0.0f;
+    for (int e = lane; e < E; e += 32) {
+        d[e] = 0.0f;
+        mx = fmaxf(mx, load_logit<T>(row + e));
     }
+    mx = warp_max(mx);
+    if (mx != -INFINITY) {
+        for (int e = lane; e < E; e += 32) sum += expf(load_logit<T>(row + e) - mx);
+        sum = warp_sum(sum);
+    }
+    const float p = have && mx != -INFINITY ? __fdiv_rn(expf(x - mx), sum) : 0.0f;
+    const float dot = warp_sum(v * p);
+    __syncwarp();
     // one choice after the other, by the lane that owns the expert: an id
     // named twice gets the sum, in the order of the choices
     for (int j = 0; j < K; ++j) {
         const int e = __shfl_sync(kFull, id, j);
-        const float gj = __shfl_sync(kFull, g, j);
-        if (e >= 0 && (e & 31) == lane) d[e] += gj;
+        const float vj = __shfl_sync(kFull, v, j);
+        if (e >= 0 && (e & 31) == lane) d[e] += vj;
     }
-    __syncwarp();
-    if (!SIGMOID && !a.renormalize)
-        for (int e = lane; e < E; e += 32) {
-            const float p = mx != -INFINITY ? __fdiv_rn(expf(load_logit<T>(row + e) - mx), sum) : 0.0f;
-            d[e] = p * (d[e] - dot);
-        }
-    __syncwarp();
-
     T* out = static_cast<T*>(a.dlogits) + tok * E;
-    if (sizeof(T) == 4) {
-        if (E % 4 == 0) {
-            for (int i = lane; i < E / 4; i += 32)
-                st_v4(reinterpret_cast<uint4*>(out) + i, reinterpret_cast<const uint4*>(d)[i]);
-        } else {
-            for (int e = lane; e < E; e += 32) reinterpret_cast<float*>(out)[e] = d[e];
-        }
-    } else if (E % 8 == 0) {
-        for (int i = lane; i < E / 8; i += 32) {
-            const float4 u = reinterpret_cast<const float4*>(d)[2 * i], w = reinterpret_cast<const float4*>(d)[2 * i + 1];
-            st_v4(reinterpret_cast<uint4*>(out) + i,
-                  make_uint4(f32x2_to_bf16x2(u.x, u.y), f32x2_to_bf16x2(u.z, u.w), f32x2_to_bf16x2(w.x, w.y),
-                             f32x2_to_bf16x2(w.z, w.w)));
-        }
-    } else {
-        for (int e = lane; e < E; e += 32) reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(d[e]);
+    for (int e = lane; e < E; e += 32) {                     // the lane's own entries
+        const float pe = mx != -INFINITY ? __fdiv_rn(expf(load_logit<T>(row + e) - mx), sum) : 0.0f;
+        const float f = pe * (d[e] - dot);
+        if (sizeof(T) == 4) reinterpret_cast<float*>(out)[e] = f;
+        else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(f);
     }
 }
 
@@ -620,13 +653,23 @@ cudaError_t launch_moe_gate_backward(const void* logits, int f32, const int32_t*
                                      int64_t tokens, int experts, int sigmoid, int topk, int renormalize,
                                      float scale, void* dlogits, uint32_t* err, cudaStream_t st) {
     const GateBwdArgs a{logits, ids, dweights, tokens, experts, topk, renormalize, scale, dlogits, err};
-    const dim3 grid((unsigned)((tokens + kGateWarps - 1) / kGateWarps)), block(32 * kGateWarps);
-    const size_t smem = (size_t)kGateWarps * ((experts + 3) / 4 * 4) * sizeof(float);
+    const auto launch = [&](auto kernel, int per_warp, size_t smem) {
+        const int64_t per = kGateWarps * per_warp;
+        return launch_pdl(kernel, dim3((unsigned)((tokens + per - 1) / per)), dim3(32 * kGateWarps), smem, st, a);
+    };
+    if (!sigmoid && !renormalize) {
+        const size_t smem = (size_t)kGateWarps * ((experts + 3) / 4 * 4) * sizeof(float);
+        return f32 ? launch(moe_gate_bwd_dense_kernel<float>, 1, smem) : launch(moe_gate_bwd_dense_kernel<uint16_t>, 1, smem);
+    }
+    // four tokens per warp where their choices fit: a quarter of the instructions
+    if (topk <= 8) {
+        if (f32)
+            return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 8>, 4, 0) : launch(moe_gate_bwd_kernel<float, false, 8>, 4, 0);
+        return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 8>, 4, 0) : launch(moe_gate_bwd_kernel<uint16_t, false, 8>, 4, 0);
+    }
     if (f32)
-        return sigmoid ? launch_pdl(moe_gate_bwd_kernel<float, true>, grid, block, smem, st, a)
-                       : launch_pdl(moe_gate_bwd_kernel<float, false>, grid, block, smem, st, a);
-    return sigmoid ? launch_pdl(moe_gate_bwd_kernel<uint16_t, true>, grid, block, smem, st, a)
-                   : launch_pdl(moe_gate_bwd_kernel<uint16_t, false>, grid, block, smem, st, a);
+        return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 32>, 1, 0) : launch(moe_gate_bwd_kernel<float, false, 32>, 1, 0);
+    return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 32>, 1, 0) : launch(moe_gate_bwd_kernel<uint16_t, false, 32>, 1, 0);
 }
 
 }  // namespace fpq
