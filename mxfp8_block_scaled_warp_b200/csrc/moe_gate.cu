@@ -58,14 +58,6 @@ __device__ __forceinline__ float value(uint32_t p) {
     return __uint_as_float((p & 0x80000000u) ? p ^ 0x80000000u : ~p);
 }
 
-// At least twice the error of a sum of `n` fp32 keys near `key`.  An fp32
-// score (at most 1) is within 2^-18: exp and the division within a few units
-// in the last place, the softmax's sum of up to 1024 terms (at most 37
-// additions in a row) within 2^-18.7 of its value.
-__device__ __forceinline__ float slack(float key, int n) {
-    return fabsf(key) < INFINITY ? (float)n * 0x1p-17f * (1.0f + fabsf(key)) : 0.0f;
-}
-
 template <typename T> __device__ __forceinline__ float load_logit(const T* p);
 template <> __device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
 template <> __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
@@ -73,7 +65,8 @@ template <> __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
-// For keys: within 2^-20, what `slack` allows for.
+// For keys: within 2^-21 (the fast exponential's error grows with its
+// argument, which the sigmoid's slope outweighs).
 __device__ __forceinline__ float sigmoid_key(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -161,6 +154,14 @@ moe_gate_kernel(const GateArgs a) {
         if (mx == -INFINITY) return x == x ? 0.0f : x;
         return __fdividef(__expf(x - mx), sum);
     };
+    // At least twice the error of a sum of n fp32 keys near `key`: a sigmoid is
+    // within 2^-20; a softmax within 2^-18 of the row's largest (1 / sum), as
+    // its sum of up to 1024 terms goes through at most 37 additions in a row;
+    // adding the bias costs half a step.
+    const float error = SIGMOID ? 0x1p-20f : sum > 0.0f ? __fdividef(0x1p-18f, sum) : 0.0f;
+    const auto slack = [&](float key, int n) {
+        return fabsf(key) < INFINITY ? 2.0f * (float)n * (error + 0x1p-23f * fabsf(key)) : 0.0f;
+    };
     double sum64 = 0.0;
     const auto need64 = [&]() {                             // warp-uniform
         if (!SIGMOID && sum64 == 0.0 && mx != -INFINITY) {
@@ -191,11 +192,11 @@ moe_gate_kernel(const GateArgs a) {
         __syncwarp();
         // `split` adjacent lanes share a group; lane `split` g holds its rank:
         // its largest key, or the sum of its two largest
-        const int size = E / a.n_group, split = 32 >> (32 - __clz(a.n_group - 1)), g = lane / split;
+        const int size = E / a.n_group, shift = __clz(a.n_group - 1) - 27, split = 1 << shift, g = lane >> shift;
         float first = -INFINITY, second = -INFINITY;
         if (g < a.n_group)
 #pragma unroll 4
-            for (int e = g * size + lane % split; e < (g + 1) * size; e += split) {
+            for (int e = g * size + (lane & (split - 1)); e < (g + 1) * size; e += split) {
                 const float v = s[e + (e >> 5)];
                 second = fmaxf(second, fminf(first, v));    // a NaN is passed over
                 first = fmaxf(first, v);
@@ -206,7 +207,7 @@ moe_gate_kernel(const GateArgs a) {
             first = fmaxf(first, f);
         }
         const float rank = a.group_top == 2 ? first + second : first;
-        const bool holds = g < a.n_group && lane % split == 0;
+        const bool holds = g < a.n_group && (lane & (split - 1)) == 0;
         uint32_t gkey = holds ? pattern(rank) : kTaken;
         uint32_t open = 0;                                   // chosen groups
         for (int c = 0; c < a.topk_group; ++c) {
@@ -216,18 +217,31 @@ moe_gate_kernel(const GateArgs a) {
             const uint32_t cand = __ballot_sync(kFull, near);
             int best = __ffs(cand) - 1;
             if (cand & (cand - 1)) {
+                // the near groups' ranks in fp64, one after the other, over the warp
                 need64();
-                double f = -INFINITY, n = -INFINITY;
-                if (near)
+                double most = 0.0;
+                best = -1;
+                for (uint32_t left = cand; left; left &= left - 1) {
+                    const int holder = __ffs(left) - 1, at = (holder >> shift) * size;
+                    double f = -INFINITY, n = -INFINITY;
 #pragma unroll 1
-                    for (int e = g * size; e < (g + 1) * size; ++e) {
+                    for (int e = at + lane; e < at + size; e += 32) {
                         const double v = key64(e);
                         if (v > f) { n = f; f = v; }
                         else if (v > n) n = v;
                     }
-                best = best64(a.group_top == 2 ? f + n : f, lane, near);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const double F = __shfl_xor_sync(kFull, f, o), N = __shfl_xor_sync(kFull, n, o);
+                        n = fmax(fmax(n, N), fmin(f, F));
+                        f = fmax(f, F);
+                    }
+                    double r = a.group_top == 2 ? f + n : f;
+                    if (!(r == r)) r = -INFINITY;
+                    if (best < 0 || r > most) { best = holder; most = r; }   // equal ones: the lowest group
+                }
             }
-            open |= 1u << (best / split);
+            open |= 1u << (best >> shift);
             if (lane == best) gkey = kTaken;
         }
         // e / size for e < 1024: the reciprocal is off by less than e / 2^20 < 1 / size
