@@ -46,7 +46,7 @@ namespace {
 constexpr int kGemvWarps = 16;             // of an SM, in one CTA or two
 constexpr int kBlock = 128;               // weights of a row per warp and step
 constexpr int kGroup = 4;                 // blocks per group
-constexpr int kXBytes = 112 * 1024;       // of an SM for x, unless a CTA's warps need more for a group each
+constexpr int kXBytes = 112 * 1024;       // of an SM for x
 
 struct GemvArgs {
     const uint16_t* x;          // row m at x + (m / x_div) k
@@ -63,7 +63,7 @@ struct GemvArgs {
     int y_f32;
     int cap;                    // pairs of an expert that a CTA takes (at most the columns)
     int wk, wr;                 // warps along k, row tiles per CTA
-    int chunk;                  // groups of x in shared memory at a time, a multiple of wk
+    int chunk;                  // groups of x in shared memory at a time
 };
 
 __device__ __forceinline__ void put(void* y, int64_t at, float v, bool f32) {
@@ -267,7 +267,7 @@ gemv_nvfp4_kernel(const GemvArgs a) {
         stage(group0);
         __syncthreads();
         const int last = min(groups - group0, a.chunk);
-        for (int gl = wk; gl < last; gl += WK) {
+        for (int gl = (wk - group0 % WK + WK) % WK; gl < last; gl += WK) {   // groups wk, wk + WK, ... of all
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 uint32_t sc[2][2];                           // [row][scale]
@@ -332,8 +332,8 @@ gemv_nvfp4_kernel(const GemvArgs a) {
 template <int TILES, int CTAS>
 cudaError_t gemv(GemvArgs a, cudaStream_t st) {
     const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock), cols = a.ids ? a.cap : a.m;
-    const int fit = kXBytes / CTAS / (cols * kGroup * 256) / a.wk * a.wk, all = (groups + a.wk - 1) / a.wk * a.wk;
-    a.chunk = fit < a.wk ? a.wk : fit < all ? fit : all;
+    const int fit = kXBytes / CTAS / (cols * kGroup * 256);
+    a.chunk = fit < groups ? fit : groups;
     const int blocks = a.chunk * kGroup;
     const int smem = cols * (blocks * 256 + (blocks * 4 + 127) / 128 * 128 + 64);
     const auto kernel = gemv_nvfp4_kernel<TILES, CTAS>;
@@ -351,19 +351,20 @@ cudaError_t gemv(GemvArgs a, cudaStream_t st) {
 cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, const int32_t* ids, int experts,
                               const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
                               int y_f32, uint32_t* err, int sms, cudaStream_t st) {
-    // As many warps along k as leave one wave of an SM's sixteen (and a group
-    // per warp; at most eight), then as many row tiles per CTA as bring the
-    // CTAs into one wave: with 148 SMs and two CTAs each, 2048 tiles become
-    // 293 CTAs of seven warps, 128 tiles 128 CTAs of eight.  The expert form
+    // As many warps along k as leave one wave of an SM's sixteen, up to one for
+    // each group (2048 x 7168, one row: 16 warps for 14 groups 5.3 us, 8 warps
+    // 6.8), then as many row tiles per CTA as bring the CTAs into one
+    // wave: with 148 SMs and two CTAs each, 2048 tiles become 293 CTAs of
+    // seven warps; 128 tiles become 128 CTAs of sixteen.  The expert form
     // counts on eight experts per call.
     const int64_t tiles = (n + 15) / 16, waves = tiles * (ids ? 8 : 1), groups = (k + kGroup * kBlock - 1) / (kGroup * kBlock);
-    int wk = 8;
-    while (wk > 1 && (waves * wk > kGemvWarps * (int64_t)sms || groups < wk)) wk /= 2;
+    int wk = kGemvWarps;
+    while (wk > 1 && (waves * wk > kGemvWarps * (int64_t)sms || wk / 2 >= groups)) wk /= 2;
     // Sixteen columns for more than eight rows, or where an expert can be
     // expected to have more than eight pairs.  Then one CTA per SM: x fills
     // its shared memory, and is converted once for twice the weights.
     const bool wide = ids ? m > 8 && m > 4 * (int64_t)experts : m > 8;
-    const int ctas = wide ? 1 : 2;
+    const int ctas = wide || wk == kGemvWarps ? 1 : 2;
     const int64_t wr = max64(1, min64(kGemvWarps / ctas / wk, (waves + ctas * sms - 1) / (ctas * sms)));
     // An expert has at most a pair of each token (of a token that names it
     // twice, two).  Four where that is far above the average: they take half
@@ -371,7 +372,7 @@ cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, c
     const int cap = wide ? 16 : tokens < 4 ? tokens : m <= 2 * (int64_t)experts ? 4 : 8;
     const GemvArgs a{(const uint16_t*)x, (int)m, x_div, ids, experts, (const uint8_t*)wq, (const uint8_t*)ws, wg, n,
                      (int)k, y, err, y_f32, cap, wk, (int)wr, 0};
-    return wide ? gemv<2, 1>(a, st) : gemv<1, 2>(a, st);
+    return wide ? gemv<2, 1>(a, st) : ctas == 1 ? gemv<1, 1>(a, st) : gemv<1, 2>(a, st);
 }
 
 }  // namespace fpq
