@@ -44,6 +44,7 @@ def sources() -> list[str]:
 
 def _headers() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  glob.glob(os.path.join(CSRC, "*.hpp")) +
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 

@@ -9,6 +9,7 @@
 
 #include "../../include/fpq.h"
 #include "internal.h"
+#include "layer.hpp"
 
 namespace {
 

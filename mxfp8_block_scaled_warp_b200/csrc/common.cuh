@@ -58,14 +58,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t c) {
     return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
 }
 
-// two E4M3 codes (bits 0..15) -> packed f16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c2) {
-    uint32_t h2;
-    uint16_t in = (uint16_t)(c2 & 0xFFFFu);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
-    return h2;
-}
-
 // two E4M3 codes (bits 0..15) -> two fp32, exact.
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t c2) {
     uint32_t h2;

@@ -36,7 +36,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "layer.hpp"
 #include "quant_unit.cuh"
 
 namespace fpq {

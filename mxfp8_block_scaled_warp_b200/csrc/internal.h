@@ -108,42 +108,6 @@ cudaError_t launch_grouped_gemm_mxfp8(const void* aq, const void* as, const void
                                       int64_t total_m, int64_t n, int64_t k, void* c, int c_f32,
                                       uint32_t* err, int sms, cudaStream_t st);
 
-// RMS norm (rmsnorm.cu): fmt FPQ_FP8_1x128 or FPQ_MXFP8 when q is given;
-// residual, h, y, q + scales and rstd may be nullptr.  ld_x in elements.
-cudaError_t launch_rmsnorm_quantize(int fmt, const void* x, int64_t ld_x, const void* residual, const void* weight,
-                                    int64_t rows, int64_t cols, float eps, void* h, void* y, void* q, void* scales,
-                                    float* rstd, int sms, cudaStream_t st);
-size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, int sms);
-cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight,
-                                    const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
-                                    float* dweight, void* workspace, uint32_t* err, int sms, cudaStream_t st);
-
-// Expert gate (moe_gate.cu): f32 selects fp32 logits, else bf16.
-cudaError_t launch_moe_gate(const void* logits, int f32, const float* bias, int64_t tokens, int experts, int sigmoid,
-                            int n_group, int topk_group, int group_top, int topk, int renormalize, float scale,
-                            int32_t* ids, float* weights, cudaStream_t st);
-cudaError_t launch_moe_gate_backward(const void* logits, int f32, const int32_t* ids, const float* dweights,
-                                     int64_t tokens, int experts, int sigmoid, int topk, int renormalize,
-                                     float scale, void* dlogits, uint32_t* err, cudaStream_t st);
-
-// Combination of the experts' rows (moe_combine.cu); rows may be nullptr
-// (pair p is row p).  launch_moe_pair_rows reads the route workspace.
-cudaError_t launch_moe_pair_rows(const int32_t* ids, int64_t tokens, int topk, int experts, const void* workspace,
-                                 const int64_t* dst_row0, int32_t* rows, cudaStream_t st);
-cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const int32_t* rows, const float* weights,
-                               int64_t tokens, int topk, int64_t hidden, const void* add, void* out, int out_f32,
-                               uint32_t* err, cudaStream_t st);
-cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
-                                        const int32_t* rows, const float* weights, int64_t tokens, int topk,
-                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, int sms,
-                                        cudaStream_t st);
-
-// Few rows times NVFP4 weights (gemv_nvfp4.cu): row m of y [m, n] is row
-// m / x_div of x times the matrix (ids == nullptr) or expert ids[m]'s.
-cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, const int32_t* ids, int experts,
-                              const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
-                              int y_f32, uint32_t* err, int sms, cudaStream_t st);
-
 // Set the per-thread detail string returned by fpq_last_error_detail().
 void set_error_detail(const char* what);
 

@@ -34,7 +34,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "layer.hpp"
 
 namespace fpq {
 

@@ -24,7 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "layer.hpp"
 #include "quant_unit.cuh"
 #include "sm100.cuh"
 
@@ -276,14 +276,14 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
         const uint32_t n = (uint32_t)min64(a.batch, a.rows - row), bytes = n * row_bytes;
         uint8_t* dst = ring + stage * 3 * part;
         sm100::mbar_arrive_expect_tx(&bar[stage], bytes * (a.dres ? 3 : 2));
-        sm100::bulk_load(dst, a.dy + row * row_bytes, bytes, &bar[stage]);
+        bulk_load(dst, a.dy + row * row_bytes, bytes, &bar[stage]);
         if (a.ld == row_bytes) {
-            sm100::bulk_load(dst + part, a.x + row * row_bytes, bytes, &bar[stage]);
+            bulk_load(dst + part, a.x + row * row_bytes, bytes, &bar[stage]);
         } else {
             for (uint32_t i = 0; i < n; ++i)
-                sm100::bulk_load(dst + part + i * row_bytes, a.x + (row + i) * a.ld, row_bytes, &bar[stage]);
+                bulk_load(dst + part + i * row_bytes, a.x + (row + i) * a.ld, row_bytes, &bar[stage]);
         }
-        if (a.dres) sm100::bulk_load(dst + 2 * part, a.dres + row * row_bytes, bytes, &bar[stage]);
+        if (a.dres) bulk_load(dst + 2 * part, a.dres + row * row_bytes, bytes, &bar[stage]);
     };
     if (t == 0)
         for (int i = 0; i < a.stages; ++i) fill(first + i * teams, i);
@@ -300,7 +300,7 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     uint32_t phase = 0;
     float next_rstd = first < batches ? __ldg(a.rstd + first * a.batch) : 0.0f;
     for (int64_t b = first; b < batches; b += teams) {
-        if (!sm100::mbar_wait_seconds(&bar[stage], phase)) {     // after this long no copy is in flight
+        if (!mbar_wait_seconds(&bar[stage], phase)) {     // after this long no copy is in flight
             raise_device_error(a.err, FPQ_ERR_DEVICE_TIMEOUT);
             return;
         }

@@ -42,21 +42,6 @@ inline cudaError_t make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The same for `batch` matrices, `batch_pitch` bytes apart (box depth 1).
-inline cudaError_t make_tmap_u8_3d(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t cols,
-                                   uint64_t pitch, uint64_t batch_pitch, uint32_t box_rows, uint32_t box_cols) {
-    EncodeTiledFn fn = encode_tiled_fn();
-    if (!fn) return cudaErrorNotSupported;
-    cuuint64_t dims[3] = {cols, rows, batch};
-    cuuint64_t strides[2] = {pitch, batch_pitch};
-    cuuint32_t box[3] = {box_cols, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // General 2-D row-major tensor map: [rows, cols] elements of `elem_bytes`,
 // row pitch `pitch` bytes, box box_rows x box_cols elements.
 inline cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint32_t elem_bytes,
