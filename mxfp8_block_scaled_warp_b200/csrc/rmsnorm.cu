@@ -486,28 +486,31 @@ rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
     }
 }
 
-// dweight[c] = sum of the partial rows, in a fixed order: warp i of a CTA
-// adds rows i, i + 32, ... of its 128 columns, then the warps' sums are added.
-__global__ void __launch_bounds__(1024)
+// dweight[c] = sum of the partial rows, in a fixed order: a CTA takes 32
+// columns; thread (i, j) adds rows i, i + 32, ... of its four, then the
+// threads of a column are added in order.
+constexpr int kSumRows = 32, kSumVecs = 8;
+
+__global__ void __launch_bounds__(kSumRows * kSumVecs)
 rmsnorm_dweight_kernel(const float4* __restrict__ partial, int parts, int nvec4, float4* __restrict__ dweight) {
-    __shared__ float4 sum[32][32];
+    __shared__ float4 sum[kSumRows][kSumVecs];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int v = blockIdx.x * 32 + lane;
+    const int i = threadIdx.x / kSumVecs, j = threadIdx.x % kSumVecs, v = blockIdx.x * kSumVecs + j;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (v < nvec4) {
-#pragma unroll 4
-        for (int p = warp; p < parts; p += 32) {
+#pragma unroll 8
+        for (int p = i; p < parts; p += kSumRows) {
             const float4 u = partial[(int64_t)p * nvec4 + v];
             s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
         }
     }
-    sum[warp][lane] = s;
+    sum[i][j] = s;
     __syncthreads();
-    if (warp == 0 && v < nvec4) {
-        for (int i = 1; i < 32; ++i) {
-            const float4 u = sum[i][lane];
+    if (i == 0 && v < nvec4) {
+#pragma unroll
+        for (int r = 1; r < kSumRows; ++r) {
+            const float4 u = sum[r][j];
             s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
         }
         dweight[v] = s;
@@ -594,7 +597,8 @@ cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x,
         else e = launch_pdl(rmsnorm_bwd_long_kernel<8>, g, b, 0, st, a);
     }
     if (e != cudaSuccess || !dweight) return e;
-    return launch_pdl(rmsnorm_dweight_kernel, dim3((unsigned)((2 * nvec + 31) / 32)), dim3(1024), 0, st,
+    return launch_pdl(rmsnorm_dweight_kernel, dim3((unsigned)((2 * nvec + kSumVecs - 1) / kSumVecs)),
+                      dim3(kSumRows * kSumVecs), 0, st,
                       (const float4*)workspace, grid, 2 * nvec, (float4*)dweight);
 }
 
