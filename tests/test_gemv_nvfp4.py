@@ -42,7 +42,7 @@ def _x(shape, seed):
 
 
 @pytest.mark.parametrize("n,k", [(1, 32), (7, 64), (16, 96), (33, 544), (128, 512), (100, 2048), (2048, 7168),
-                                 (5001, 1056), (40, 16384), (300, 14336)])
+                                 (5001, 1056), (40, 16384), (300, 14336), (20011, 544)])
 @pytest.mark.parametrize("m", [1, 2, 7, 8, 9, 16])
 def test_dense(fpq, n, k, m):
     wq, ws, wg = _weights(fpq, (n, k), n + k)
@@ -168,3 +168,21 @@ def test_no_rows(fpq):
     assert fpq.gemv_nvfp4(x, wq[0], ws[0], wg[:1]).shape == (0, 16)
     ids = torch.empty((0, 2), dtype=torch.int32, device="cuda")
     assert fpq.gemv_nvfp4(x, wq, ws, wg, ids=ids).shape == (0, 2, 16)
+
+
+def test_far_experts(fpq):
+    """Codes and scales past 2^32 bytes from the first."""
+    experts, n, k = 640, 2048, 7168
+    wq = torch.empty((experts, n, k // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.empty((experts, n, k // 16), dtype=torch.uint8, device="cuda")
+    wg = torch.ones((experts,), device="cuda")
+    assert wq.numel() > 2 ** 32
+    used = [0, 584, 585, 586, experts - 1]                   # 2^32 bytes of codes end inside expert 585
+    for e in used:
+        q, s, g = _weights(fpq, (n, k), e)
+        wq[e], ws[e], wg[e] = q, s, g[0]
+    x = _x((1, k), 3)
+    ids = torch.tensor([used], dtype=torch.int32, device="cuda")
+    y = fpq.gemv_nvfp4(x, wq, ws, wg, ids=ids, out_dtype=torch.float32)
+    for j, e in enumerate(used):
+        _inside(y[:, j], x.double(), _decode(wq[e], ws[e], wg[e:e + 1])[None], torch.float32)

@@ -140,3 +140,32 @@ def test_no_tokens(fpq):
     assert moe.combine(y, w).shape == (0, 64)
     dy, dw = moe.combine_backward(y, y, w)
     assert dy.shape == (0, 64) and dw.shape == (0, 4)
+
+
+def test_far_rows(fpq):
+    """Rows past 2^31 elements from the first."""
+    hidden, y_rows = 7168, 310000
+    y = torch.zeros((y_rows, hidden), dtype=torch.bfloat16, device="cuda")
+    y[-8:] = torch.randn((8, hidden), device="cuda").to(torch.bfloat16)
+    rows = torch.arange(y_rows - 8, y_rows, dtype=torch.int32, device="cuda").view(2, 4)
+    w = torch.rand((2, 4), device="cuda")
+    near = y[-8:].clone()
+    assert torch.equal(moe.combine(y, w, rows=rows), moe.combine(near, w))
+    dout = torch.randn((2, hidden), device="cuda").to(torch.bfloat16)
+    dy, dw = moe.combine_backward(dout, y, w, rows=rows)
+    dy_near, dw_near = moe.combine_backward(dout, near, w)
+    assert torch.equal(dy[-8:], dy_near) and torch.equal(dw, dw_near)
+
+
+def test_many_tokens_without_a_row_map(fpq):
+    y, _, w, add = _case(2600, 8, 64, 13, torch.bfloat16)
+    rows = torch.arange(2600 * 8, dtype=torch.int32, device="cuda").view(2600, 8)
+    rows[5, 3] = -1
+    rows[2599] = -1
+    dout = torch.randn((2600, 64), device="cuda").to(torch.bfloat16)
+    dy, dw = moe.combine_backward(dout, y, w, rows=rows, dy=torch.zeros_like(y))
+    full_dy, full_dw = moe.combine_backward(dout, y, w)
+    keep = (rows >= 0)
+    assert torch.equal(dw[keep], full_dw[keep]) and torch.all(dw[~keep] == 0)
+    assert torch.equal(dy.view(2600, 8, 64)[keep], full_dy.view(2600, 8, 64)[keep])
+    assert torch.all(dy.view(2600, 8, 64)[~keep] == 0)

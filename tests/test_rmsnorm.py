@@ -225,3 +225,49 @@ def test_same_as_quantizing_the_rows_of_a_product(fpq):
     out = fpq.rmsnorm_quantize(x * 2, w, fpq.MXFP8, eps=2.0)                       # rstd = 1 / 2
     q, s = fpq.quantize(x, fpq.MXFP8)
     assert torch.equal(out.q, q) and torch.equal(out.scales, s)
+
+
+@pytest.mark.parametrize("rows,cols", [(700, 40), (2000, 1024), (900, 2048), (500, 7168), (310, 16384), (310, 16392)])
+@pytest.mark.parametrize("over", ["dy", "dres"])
+def test_backward_in_place(fpq, rows, cols, over):
+    x, w, _ = _data(rows, cols, 31)
+    dy, dres = (torch.randn((rows, cols), device="cuda").to(BF16) for _ in range(2))
+    rstd = _ref(x, w, None, 1e-6)[1].float()
+    want = fpq.rmsnorm_backward(dy, x, w, rstd, dres=dres)
+    buf = {"dy": dy, "dres": dres}
+    dw = torch.empty((cols,), device="cuda")
+    ws = torch.empty((fpq.fpq_rmsnorm_backward_workspace_bytes(rows, cols),), dtype=torch.uint8, device="cuda")
+    fpq.fpq_rmsnorm_backward(dy, x, cols, w, rstd, dres, rows, cols, buf[over], dw, ws)
+    assert torch.equal(buf[over], want[0]) and torch.equal(dw, want[1])
+
+
+def test_without_a_weight_gradient(fpq):
+    x, w, _ = _data(33, 512, 32)
+    dy = torch.randn((33, 512), device="cuda").to(BF16)
+    rstd = _ref(x, w, None, 1e-6)[1].float()
+    dx = torch.empty_like(dy)
+    fpq.fpq_rmsnorm_backward(dy, x, 512, w, rstd, None, 33, 512, dx)
+    assert torch.equal(dx, fpq.rmsnorm_backward(dy, x, w, rstd)[0])
+
+
+def test_far_rows(fpq):
+    """Rows past 2^32 bytes and 2^31 elements from the first, dense and strided."""
+    rows, cols = 330000, 8192
+    x = torch.zeros((rows, cols), dtype=BF16, device="cuda")
+    part, w, _ = _data(64, cols, 33)
+    x[-64:] = part
+    out = fpq.rmsnorm_quantize(x, w, fpq.MXFP8, want_y=True, want_rstd=True)
+    _, rstd, y = _ref(part, w, None, 1e-6)
+    _near(out.rstd[-64:], rstd, F32_REL)
+    _near(out.y[-64:], y, 2.0 ** -8 + F32_REL)
+    _check_codes(fpq, fpq.MXFP8, out.q[-64:], out.scales[-64:], y)
+    half = fpq.rmsnorm_quantize(x[:, :4096], w[:4096].contiguous(), want_rstd=True)
+    _near(half.y[-64:], _ref(part[:, :4096], w[:4096], None, 1e-6)[2], 2.0 ** -8 + F32_REL)
+    dx, dw = fpq.rmsnorm_backward(out.y, x, w, out.rstd)
+    dy, rstd = out.y[-64:].clone(), out.rstd[-64:].clone()
+    dx_near, dw_near = fpq.rmsnorm_backward(dy, part.contiguous(), w, rstd)
+    assert torch.equal(dx[-64:], dx_near)
+    # the other rows add zeros; the same 64 products are added in two orders,
+    # each within 64 steps of 2^-24 of the magnitudes' sum
+    size = (dy.double() * part.double() * rstd.double()[:, None]).abs().sum(0)
+    assert torch.all((dw.double() - dw_near.double()).abs() <= 2.0 ** -17 * size)
