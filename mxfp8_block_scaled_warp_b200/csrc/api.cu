@@ -621,7 +621,7 @@ fpq_status fpq_moe_gate(const void* logits, int32_t logits_dtype, const float* b
                         int32_t topk, int32_t renormalize, float scale, int32_t* ids, float* weights, void* stream) {
     t_detail[0] = 0;
     fpq_status st;
-    if (tokens < 0 || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || topk > num_experts ||
+    if (tokens < 0 || tokens > INT32_MAX || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || topk > num_experts ||
         tokens * topk >= (1ll << 31) || (logits_dtype != FPQ_OUT_BF16 && logits_dtype != FPQ_OUT_F32) ||
         (score != FPQ_MOE_SOFTMAX && score != FPQ_MOE_SIGMOID) || (renormalize != 0 && renormalize != 1)) {
         set_detail("need tokens >= 0, num_experts in [1, 1024], topk in [1, min(32, num_experts)], tokens * topk < "
@@ -651,7 +651,7 @@ fpq_status fpq_moe_gate_backward(const void* logits, int32_t logits_dtype, const
                                  int32_t renormalize, float scale, void* dlogits, void* stream) {
     t_detail[0] = 0;
     fpq_status st;
-    if (tokens < 0 || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) ||
+    if (tokens < 0 || tokens > INT32_MAX || num_experts < 1 || num_experts > 1024 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) ||
         (logits_dtype != FPQ_OUT_BF16 && logits_dtype != FPQ_OUT_F32) ||
         (score != FPQ_MOE_SOFTMAX && score != FPQ_MOE_SIGMOID) || (renormalize != 0 && renormalize != 1)) {
         set_detail("need tokens >= 0, num_experts in [1, 1024], topk in [1, 32], tokens * topk < 2^31, bf16 or fp32 "
@@ -673,7 +673,7 @@ fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, int32_t to
                              void* stream) {
     t_detail[0] = 0;
     fpq_status st;
-    if (tokens < 0 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || num_experts < 1 ||
+    if (tokens < 0 || tokens > INT32_MAX || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || num_experts < 1 ||
         num_experts > 1024) {
         set_detail("need tokens >= 0, topk in [1, 32], tokens * topk < 2^31, num_experts in [1, 1024]");
         return FPQ_ERR_INVALID_ARG;
@@ -695,10 +695,10 @@ fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, int32_t to
 namespace {
 fpq_status check_combine(int64_t y_rows, const int32_t* rows, int64_t tokens, int32_t topk, int64_t hidden,
                          int32_t y_dtype, int32_t o_dtype) {
-    if (tokens < 0 || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || hidden < 8 || hidden % 8 ||
+    if (tokens < 0 || tokens > INT32_MAX || topk < 1 || topk > 32 || tokens * topk >= (1ll << 31) || hidden < 8 || hidden % 8 ||
         hidden > (1 << 24) || y_rows < 0 || y_rows >= (1ll << 31) ||
         (y_dtype != FPQ_OUT_BF16 && y_dtype != FPQ_OUT_F32) || (o_dtype != FPQ_OUT_BF16 && o_dtype != FPQ_OUT_F32)) {
-        set_detail("need tokens >= 0, topk in [1, 32], tokens * topk < 2^31, hidden a positive multiple of 8, "
+        set_detail("need tokens >= 0, topk in [1, 32], tokens * topk < 2^31, hidden a positive multiple of 8 up to 2^24, "
                    "0 <= y_rows < 2^31, bf16 or fp32 types");
         return FPQ_ERR_INVALID_ARG;
     }

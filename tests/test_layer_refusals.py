@@ -171,3 +171,12 @@ def test_python_entry_points():
         with pytest.raises(ValueError):
             call()
             raise AssertionError(f"call {i} was not refused")
+
+
+def test_counts_whose_product_passes_64_bits(lib):
+    far = 1 << 62
+    assert lib.fpq_moe_gate(P, 1, P, far, 64, 1, 8, 4, 2, 8, 1, 1.0, P, P, None) == INVALID
+    assert lib.fpq_moe_gate_backward(P, 0, P, P, far, 64, 0, 8, 1, 1.0, P, None) == INVALID
+    assert lib.fpq_moe_combine(P, 0, 128, P, P, far, 8, 64, P, P, 0, None) == INVALID
+    assert lib.fpq_moe_combine_backward(P, 1, P, 0, 128, P, P, far, 8, 64, P, P, None) == INVALID
+    assert lib.fpq_moe_pair_rows(P, far, 8, 64, P, 1 << 30, P, P, None) == INVALID
