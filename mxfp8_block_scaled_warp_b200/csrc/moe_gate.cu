@@ -3,11 +3,11 @@
 // optional group-limited choice, top-k, and the routing weights.
 //
 //   score p_e = softmax(l)_e or 1 / (1 + exp(-l_e))
-//   key     k_e = l_e without a bias (both scores grow with the logit),
-//               p_e + b_e with one
+//   key     k_e = l_e without a bias (both scores grow with the logit) and
+//               where l_e is -inf, p_e + b_e with one
 //   groups: E / n_group consecutive experts each; a group's rank is the sum
-//           of its `group_top` largest keys (of p without a bias); experts
-//           outside the topk_group best groups are not chosen
+//           of its `group_top` largest p_e + b_e (p_e without a bias);
+//           experts outside the topk_group best groups are not chosen
 //   ids     the topk largest keys, in order; equal keys by lowest index
 //   weights scale p_e, divided by the sum of the chosen p with `renormalize`
 //
@@ -44,9 +44,9 @@ constexpr int kGateWarps = 4;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // Order-preserving patterns: larger key, larger pattern.  Below every number
-// (-inf is 0x007FFFFF): NaN 2, outside the chosen groups 1, taken or past
+// (-inf is kMasked): NaN 2, outside the chosen groups 1, taken or past
 // the last expert 0.
-constexpr uint32_t kTaken = 0, kOutside = 1, kNaN = 2;
+constexpr uint32_t kTaken = 0, kOutside = 1, kNaN = 2, kMasked = 0x007FFFFF;
 
 __device__ __forceinline__ uint32_t pattern(float f) {
     if (f != f) return kNaN;
@@ -175,20 +175,22 @@ moe_gate_kernel(const GateArgs a) {
         return a.bias ? p + (double)__ldg(a.bias + e) : p;
     };
 
+    float* const s = sh + warp * (E + E / 32 + 1);          // entry e at e + e / 32: a group's scan is free of conflicts
     uint32_t key[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int e = 32 * i + lane;
-        key[i] = e >= E ? kTaken : pattern(a.bias ? score_key(l[i]) + __ldg(a.bias + e) : l[i]);
+        float k = l[i];
+        if (scores && e < E) {
+            float r = score_key(l[i]);
+            if (a.bias) r += __ldg(a.bias + e);
+            if (a.bias && l[i] != -INFINITY) k = r;          // a masked expert gains nothing by its bias
+            if (a.n_group > 1) s[e + i] = r == r ? r : -INFINITY;
+        }
+        key[i] = e >= E ? kTaken : pattern(k);
     }
 
     if (a.n_group > 1) {
-        float* s = sh + warp * (E + E / 32 + 1);            // entry e at e + e / 32: a group's scan is free of conflicts
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int e = 32 * i + lane;
-            if (e < E) s[e + i] = a.bias ? value(key[i]) : score_key(l[i]);
-        }
         __syncwarp();
         // `split` adjacent lanes share a group; lane `split` g holds its rank:
         // its largest key, or the sum of its two largest
@@ -198,7 +200,7 @@ moe_gate_kernel(const GateArgs a) {
 #pragma unroll 4
             for (int e = g * size + (lane & (split - 1)); e < (g + 1) * size; e += split) {
                 const float v = s[e + (e >> 5)];
-                second = fmaxf(second, fminf(first, v));    // a NaN is passed over
+                second = fmaxf(second, fminf(first, v));
                 first = fmaxf(first, v);
             }
         for (int o = 1; o < split; o <<= 1) {
@@ -301,7 +303,7 @@ moe_gate_kernel(const GateArgs a) {
         }
         if (__any_sync(kFull, near && lane < count)) {
             need64();
-            double k64 = lane < count ? key64(mine) : 0.0;
+            double k64 = c.x > kMasked ? key64(mine) : -INFINITY;
             if (!(k64 == k64)) k64 = -INFINITY;
             // NaN patterns are behind every number
             const int group = c.x > kNaN;

@@ -245,3 +245,43 @@ def test_no_tokens(fpq):
     ids, w = moe.gate(lg, 8)
     assert ids.shape == w.shape == (0, 8)
     assert moe.gate_backward(w, lg, ids).shape == (0, 64)
+
+
+@pytest.mark.parametrize("score", [moe.SOFTMAX, moe.SIGMOID])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_masked_experts_do_not_gain_by_their_bias(fpq, score, grouped):
+    """With a bias, too, a -inf logit is chosen after every other expert."""
+    lg = _logits(120, 64, 21)
+    g = torch.Generator().manual_seed(22)
+    lg[torch.rand((120, 64), generator=g).cuda() < 0.5] = -math.inf
+    lg[0, 3:] = -math.inf
+    lg[1, 1:] = -math.inf
+    lg[2] = -math.inf
+    bias = torch.where(torch.arange(64, device="cuda") % 3 == 0, 2.0, -0.5)
+    kw = dict(n_group=4, topk_group=2, group_top=2) if grouped else {}
+    for topk in (1, 6, 32):
+        ids, w = moe.gate(lg, topk, bias=bias, score=score, **kw)
+        masked = lg.gather(1, ids.long()) == -math.inf
+        assert torch.all(masked.int().diff(dim=1) >= 0)          # masked ones last
+        assert torch.all(w[masked] == 0)
+        for t in range(120):
+            allowed = torch.isfinite(lg[t])
+            if grouped:
+                score_t = _scores(lg[t:t + 1].double(), score)[0] + bias.double()
+                rank = score_t.view(4, 16).topk(2, 1).values.sum(1)
+                best = torch.sort(rank, descending=True, stable=True).indices[:2]
+                allowed &= torch.isin(torch.arange(64, device="cuda") // 16, best)
+                assert torch.all(torch.isin(ids[t] // 16, best))
+            assert (~masked[t]).sum().item() == min(topk, allowed.sum().item())
+        assert torch.all(ids.sort(1).values.diff(dim=1) > 0)
+
+
+def test_groups_pass_over_a_nan(fpq):
+    """A NaN logit does not count toward its group's rank."""
+    at = lambda p: math.log(p / (1 - p))
+    lg = torch.full((2, 8), at(0.05), device="cuda")
+    lg[:, 0], lg[:, 1], lg[:, 2] = at(0.9), at(0.1), math.nan        # 1.0
+    lg[:, 4], lg[:, 5] = at(0.7), at(0.6)                            # 1.3
+    lg[1, 2], lg[1, 0] = at(0.9), math.nan                           # before and behind the others
+    ids, _ = moe.gate(lg, 2, score=moe.SIGMOID, n_group=2, topk_group=1, group_top=2)
+    assert torch.equal(ids.cpu(), torch.tensor([[4, 5], [4, 5]], dtype=torch.int32))
