@@ -27,8 +27,6 @@ import os
 from typing import NamedTuple
 
 import torch
-from torch._C import _cuda_getCurrentRawStream as _raw_stream
-from torch.cuda import current_device as _device_index
 
 __all__ = [
     "FP8_1x128", "FP8_128x128", "MXFP8", "NVFP4", "OUT_BF16", "OUT_F32", "FpqError", "lib_path", "load",
@@ -146,7 +144,8 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return _raw_stream(_device_index())     # torch.cuda.current_stream() builds a Stream object: 3 us
+        # torch.cuda.current_stream() builds a Stream object: 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 

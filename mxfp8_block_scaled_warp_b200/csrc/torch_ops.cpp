@@ -155,7 +155,7 @@ py::tuple moe_gate(const Tensor& logits, int topk, const OptTensor& bias, int sc
     const int32_t type = out_type(logits.scalar_type());
     const int64_t tokens = logits.size(0), experts = logits.size(1);
     need(!bias || is(*bias, at::kFloat, {experts}), "need bias fp32 [E]");
-    need(topk >= 0 && experts <= INT32_MAX, "need topk >= 1");
+    need(topk >= 1 && topk <= experts && experts <= INT32_MAX, "need topk in [1, E]");
     need(logits.is_contiguous(), "tensors passed to the library must be contiguous");
     Call call(logits, {ptr(bias)});
     Tensor ids = empty(logits, {tokens, topk}, at::kInt), weights = empty(logits, {tokens, topk}, at::kFloat);

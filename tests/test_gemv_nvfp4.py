@@ -186,3 +186,17 @@ def test_far_experts(fpq):
     y = fpq.gemv_nvfp4(x, wq, ws, wg, ids=ids, out_dtype=torch.float32)
     for j, e in enumerate(used):
         _inside(y[:, j], x.double(), _decode(wq[e], ws[e], wg[e:e + 1])[None], torch.float32)
+
+
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 8, 4), (1, 32, 2), (2, 5, 3), (3, 32, 1), (33, 31, 2), (5, 8, 40)])
+def test_experts_named_several_times(fpq, tokens, topk, experts):
+    """A token that names an expert more than once, and every pair naming one."""
+    wq, ws, wg = _weights(fpq, (experts, 40, 160), 14)
+    x = _x((tokens, topk, 160), 15)
+    w = _decode(wq, ws, wg)
+    g = torch.Generator().manual_seed(16)
+    for ids in (torch.zeros((tokens, topk)), torch.full((tokens, topk), experts - 1),
+                torch.randint(0, min(experts, 3), (tokens, topk), generator=g)):
+        ids = ids.int().cuda()
+        y = fpq.gemv_nvfp4(x, wq, ws, wg, ids=ids, out_dtype=torch.float32)
+        _inside(y, x.double(), w[ids.long()], torch.float32)
