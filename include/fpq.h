@@ -517,7 +517,8 @@ FPQ_API fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const
  *   rstd       fp32 [rows] (optional output, kept for the backward pass)
  *
  * At least one of y and q.  The codes are those of y before its rounding to
- * bf16.  Other overlaps between inputs and outputs are not allowed.
+ * bf16 (FP8_1x128: of y times the scale's fp32 reciprocal, within 2^-23 of the
+ * quotient).  Other overlaps between inputs and outputs are not allowed.
  *
  * Requires 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768] (of 128 with
  * FPQ_FP8_1x128 codes, of 32 with FPQ_MXFP8), ld_x >= cols a multiple of 8,
@@ -562,10 +563,12 @@ FPQ_API fpq_status fpq_rmsnorm_backward(const void* dy, const void* x, int64_t l
  * logits: what fpq_moe_route and fpq_moe_dispatch_mxfp8 take as topk_ids.
  *   score_e  softmax(logits)_e (FPQ_MOE_SOFTMAX) or 1 / (1 + exp(-logit_e))
  *            (FPQ_MOE_SIGMOID)
- *   key_e    logit_e without a bias, score_e + bias_e with one
+ *   key_e    logit_e without a bias and where it is -inf, score_e + bias_e
+ *            with one
  *   groups   n_group runs of E / n_group consecutive experts; a group ranks by
- *            the sum of its group_top (1 or 2) largest keys (scores without a
- *            bias); only experts of the topk_group best groups are chosen
+ *            the sum of its group_top (1 or 2) largest score_e + bias_e
+ *            (score_e without a bias; a NaN counts as -inf); only experts of
+ *            the topk_group best groups are chosen
  *   ids      the topk largest keys in descending order
  *   weights  scale score_e; with renormalize divided by the sum of the
  *            chosen experts' scores (0 where that sum is 0)
@@ -622,7 +625,8 @@ FPQ_API fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, in
 /*
  * fpq_moe_combine -- the experts' rows back at their tokens:
  *   out[t] = add[t] + sum_j weights[t, j] y[rows[t, j]]
- * (j ascending, fp32 fused multiply-adds from add or zero, one rounding).
+ * (j ascending, fp32 fused multiply-adds from add or zero, one rounding).  A
+ * weight of 0 still multiplies its row (an infinity there gives NaN).
  *
  *   y        bf16 or fp32 [y_rows, hidden]: the experts' products
  *   rows     DEVICE int32 [tokens, topk] (fpq_moe_pair_rows), -1 for a
@@ -638,10 +642,11 @@ FPQ_API fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, in
  *   dy[rows[t, j]] = weights[t, j] dout[t]           (y's type and shape)
  *   dweights[t, j] = sum over hidden of dout[t] y[rows[t, j]]   (fp32)
  * A dropped pair has a zero dweight.  Rows of dy that no pair names are left
- * as they were.  A row may be named by one pair only.  dy must not overlap y.
+ * as they were.  A row may be named by one pair only.  dy must not overlap y
+ * or dout.
  *
  * Requires tokens >= 0, 1 <= topk <= 32, tokens * topk < 2^31, hidden a
- * positive multiple of 8, 0 <= y_rows < 2^31 (>= tokens * topk without rows),
+ * positive multiple of 8 up to 2^24, 0 <= y_rows < 2^31 (>= tokens * topk without rows),
  * every pointer 16-byte aligned.  Errors: FPQ_ERR_INVALID_ARG,
  * FPQ_ERR_ALIGNMENT, FPQ_ERR_CUDA.
  */
@@ -657,7 +662,9 @@ FPQ_API fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype
  * fpq_gemv_nvfp4, fpq_moe_gemv_nvfp4 -- products of a few bf16 rows with NVFP4
  * weights, the form that decoding takes (the activations stay bf16):
  *   y[m, n] = g sum_k x[m, k] e2m1(W[n, k]) e4m3(S[n, k/16])
- * Weights are decoded exactly, sums are fp32, g multiplies the sum.
+ * Weights are decoded exactly, sums are fp32, g multiplies the sum.  Elements
+ * of x are exact down to 2^-32 of the largest magnitude of their 128 (columns
+ * 128 i to 128 i + 127); smaller ones are rounded by at most 2^-40 of it.
  *
  * Dense form:
  *   x            bf16 [m, k], 0 <= m <= 16
@@ -670,8 +677,9 @@ FPQ_API fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype
  *                FPQ_ERR_DEVICE_BAD_INPUT and its row of y is zero
  *   wq, ws, wg   [E, n, k/2], [E, n, k/16], [E]
  *   y            bf16 or fp32 [tokens * topk, n]
- * Each chosen expert's weights are read once however many pairs chose it (up
- * to eight at a time).  A row's result does not depend on the other rows.
+ * Each chosen expert's weights are read once for up to 4, 8 or 16 of the pairs
+ * that chose it (the more, the more pairs there are per expert).  A row's
+ * result does not depend on the other rows.
  *
  * Requires 1 <= n <= 2^24, k a multiple of 32 in [32, 2^17], topk in [1, 32],
  * tokens * topk <= 1024, E in [1, 1024]; wg 4-byte aligned, the other pointers

@@ -28,9 +28,12 @@
 // the other: the topk-th largest of the 32 lane maxima bounds them from
 // below, the few keys at or above it (ten for eight of 256) are gathered, one
 // per lane, and each counts how many are before it, which is its place in
-// the output.  (Taking one maximum after the other: 51 us instead of the
-// figure below for 16384 tokens, 256 experts in groups; it remains for rows
-// with more than 32 such keys, which take equal logits.)
+// the output.  (Taking one maximum after the other: 51 us for 16384 tokens,
+// 256 experts in groups; it remains for rows with more than 32 such keys,
+// which take equal logits.)  Measured for eight of 256, 16384 tokens, fp32:
+// 12.5 us without a bias (1.4 TB/s), sigmoid with one 18.6, in eight groups
+// 26.7 (at 70% of the issue slots), softmax with a bias 27.4; 16 tokens in
+// groups 5.3 us, which is one warp's latency.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -385,7 +388,8 @@ moe_gate_kernel(const GateArgs a) {
 // their lists: the larger of element i of one and 7 - i of the other are the
 // eight largest of both, in bitonic order.  No step waits for the one before
 // as in taking maxima one after the other, and the four tokens of a warp
-// share the instructions: 110 per token for 64 bf16 logits.  A key carries its
+// share the instructions: 110 per token for 64 bf16 logits (16384 tokens:
+// 4.3 us; as the kernel above 9.7; 256 logits 10.9).  A key carries its
 // index, so that equal logits compare by it: in the lower half of a bf16
 // logit's pattern (which is the type's own width), else in a second word.
 template <int LANES, typename T> struct MergeKey;
@@ -518,7 +522,10 @@ __device__ __forceinline__ int checked_id(const GateBwdArgs& a, int64_t tok, int
 }
 
 // The first three: LANES lanes per token (at least topk), choice j in lane j.
-// They write zeros, 16 bytes at a time, and then the few values.
+// They write zeros, 16 bytes at a time, and then the few values.  Bound by
+// those writes and by the latency of a token's chain (its ids, their logits,
+// the sums): 16384 x 256 fp32 6.1 us, of which the zeros are 2.6; a warp per
+// token 7.8.
 template <typename T, bool SIGMOID, int LANES>
 __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_bwd_kernel(const GateBwdArgs a) {
@@ -583,7 +590,7 @@ moe_gate_bwd_kernel(const GateBwdArgs a) {
 }
 
 // The softmax over all experts: a warp per token, its row assembled in shared
-// memory.
+// memory (16384 x 256 fp32: 13.6 us, 2.5 TB/s; the exponentials bound it).
 template <typename T>
 __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_bwd_dense_kernel(const GateBwdArgs a) {

@@ -20,7 +20,13 @@
 // several CTAs per SM hide each other's reduction.  The backward keeps its
 // CTAs for the whole call (their columns' sums of dw stay in registers) and
 // so has few of them: rows travel through a ring in shared memory, bulk
-// copies three to four stages ahead.
+// copies three to four stages ahead (8192 x 7168: 78 us; with the rows loaded
+// into registers 101).
+//
+// Measured at 8192 x 7168: residual, bf16 and MXFP8 out 81 us (6.53 TB/s, the
+// rate of a copy), FP8 without bf16 68 us; backward with dres 78 us (5.98
+// TB/s; what is left is the few CTAs' waits between a row's two passes).  A
+// row of 7168 2.3 us.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
