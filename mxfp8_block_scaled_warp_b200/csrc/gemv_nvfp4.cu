@@ -72,7 +72,7 @@ struct GemvArgs {
     int y_f32;
     int cap;                    // pairs of an expert that a CTA takes (at most the columns)
     int wk, wr;                 // warps along k, row tiles per CTA
-    int chunk;                  // groups of x in shared memory at a time
+    int cols, chunk;            // columns and groups of x in shared memory at a time
 };
 
 __device__ __forceinline__ void put(void* y, int64_t at, float v, bool f32) {
@@ -136,7 +136,7 @@ template <int TILES, int CTAS>
 __global__ void __launch_bounds__(32 * kGemvWarps / CTAS, CTAS)
 gemv_nvfp4_kernel(const GemvArgs a) {
     constexpr int COLS = 8 * TILES;
-    extern __shared__ __align__(16) uint8_t smem[];         // per column: a chunk of x, then its blocks' factors
+    extern __shared__ __align__(16) uint8_t smem[];         // per column a chunk of x, then the blocks' factors
     __shared__ float red[kGemvWarps / CTAS][32][COLS / 2];
     __shared__ int member[COLS], xrow[COLS], info[2];       // info: members, occurrences before this pair
     pdl_trigger();
@@ -212,11 +212,12 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     for (int i = 0; i < kGroup; ++i) load(blk[i], wk, i);    // zeros if there is no such group
 
     // x in shared memory: column c at c x_stride; in it block b at 256 b, word
-    // j of lane t at 64 j + 16 t, and behind the chunk one fp32 factor per
-    // block.  The stride is 64 bytes past a multiple of 128, so that the
-    // eight columns of a read fall on different banks.
+    // j of lane t at 64 j + 16 t.  The stride is 64 bytes past a multiple of
+    // 128, so that the eight columns of a read fall on different banks.
+    // Behind the columns one fp32 factor per block and column.
     const int chunk_blocks = a.chunk * kGroup;
-    const int x_stride = chunk_blocks * 256 + (chunk_blocks * 4 + 127) / 128 * 128 + 64;
+    const int x_stride = chunk_blocks * 256 + 64;
+    float* const factors = reinterpret_cast<float*>(smem + a.cols * x_stride);
     // A unit is 64 bytes, the 32 elements of a lane's block; four adjacent
     // threads hold a block.
     const int col_units = chunk_blocks * 4, step_col = threads / col_units, step_u = threads % col_units;
@@ -242,8 +243,7 @@ gemv_nvfp4_kernel(const GemvArgs a) {
             const int f = top >= 0x7F80u ? -112 : top == 0 ? 0 : min(127, 141 - (int)(top >> 7));
             const uint32_t s1 = (uint32_t)(127 + f) << 7, s2 = s1 | (s1 << 16);
             if (in) {
-                uint8_t* const column = smem + col * x_stride;
-                uint8_t* const dst = column + (u >> 2) * 256 + (u & 3) * 16;
+                uint8_t* const dst = smem + col * x_stride + (u >> 2) * 256 + (u & 3) * 16;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -254,7 +254,7 @@ gemv_nvfp4_kernel(const GemvArgs a) {
                     }
                     *reinterpret_cast<uint4*>(dst + 64 * j) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if ((u & 3) == 0) reinterpret_cast<float*>(column + chunk_blocks * 256)[u >> 2] = pow2_neg(f);
+                if ((u & 3) == 0) factors[(u >> 2) * COLS + col] = pow2_neg(f);
             }
             col += step_col;
             u += step_u;
@@ -263,14 +263,11 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     };
 
     float acc[TILES][4] = {};
-    // columns past the last read the last one; their sums are not written
-    uint32_t xb[TILES], f0[TILES], f1[TILES];
+    // columns past the last read the last one, and factors that nobody wrote;
+    // their sums are not written
+    uint32_t xb[TILES];
 #pragma unroll
-    for (int h = 0; h < TILES; ++h) {
-        xb[h] = min(8 * h + g, count - 1) * x_stride + 16 * t;
-        f0[h] = min(8 * h + 2 * t, count - 1) * x_stride + chunk_blocks * 256;
-        f1[h] = min(8 * h + 2 * t + 1, count - 1) * x_stride + chunk_blocks * 256;
-    }
+    for (int h = 0; h < TILES; ++h) xb[h] = min(8 * h + g, count - 1) * x_stride + 16 * t;
     for (int group0 = 0; group0 < groups; group0 += a.chunk) {
         if (group0) __syncthreads();
         stage(group0);
@@ -309,10 +306,9 @@ gemv_nvfp4_kernel(const GemvArgs a) {
                 load(blk[i], group0 + gl + WK, i);
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
-                    const float p = *reinterpret_cast<const float*>(smem + f0[h] + gl * (kGroup * 4) + i * 4);
-                    const float q = *reinterpret_cast<const float*>(smem + f1[h] + gl * (kGroup * 4) + i * 4);
+                    const float2 f = *reinterpret_cast<const float2*>(factors + (gl * kGroup + i) * COLS + 8 * h + 2 * t);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[h][c] = fmaf(sum[h][0][c] + sum[h][1][c], c & 1 ? q : p, acc[h][c]);
+                    for (int c = 0; c < 4; ++c) acc[h][c] = fmaf(sum[h][0][c] + sum[h][1][c], c & 1 ? f.y : f.x, acc[h][c]);
                 }
             }
         }
@@ -340,11 +336,12 @@ gemv_nvfp4_kernel(const GemvArgs a) {
 
 template <int TILES, int CTAS>
 cudaError_t gemv(GemvArgs a, cudaStream_t st) {
-    const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock), cols = a.ids ? a.cap : a.m;
-    const int fit = kXBytes / CTAS / (cols * kGroup * 256);
+    const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock);
+    a.cols = a.ids ? a.cap : a.m;
+    const int fit = kXBytes / CTAS / (a.cols * kGroup * 256);
     a.chunk = fit < groups ? fit : groups;
     const int blocks = a.chunk * kGroup;
-    const int smem = cols * (blocks * 256 + (blocks * 4 + 127) / 128 * 128 + 64);
+    const int smem = a.cols * (blocks * 256 + 64) + blocks * 8 * TILES * (int)sizeof(float);
     const auto kernel = gemv_nvfp4_kernel<TILES, CTAS>;
     if (smem > 32 * 1024) {                                  // with the static arrays, past what needs no opt-in
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -380,7 +377,7 @@ cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, c
     // of the shared memory of eight, which is the loads' cache.
     const int cap = wide ? 16 : tokens < 4 ? tokens : m <= 2 * (int64_t)experts ? 4 : 8;
     const GemvArgs a{(const uint16_t*)x, (int)m, x_div, ids, experts, (const uint8_t*)wq, (const uint8_t*)ws, wg, n,
-                     (int)k, y, err, y_f32, cap, wk, (int)wr, 0};
+                     (int)k, y, err, y_f32, cap, wk, (int)wr, 0, 0};
     return wide ? gemv<2, 1>(a, st) : ctas == 1 ? gemv<1, 1>(a, st) : gemv<1, 2>(a, st);
 }
 
