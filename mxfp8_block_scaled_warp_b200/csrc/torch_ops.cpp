@@ -2,10 +2,11 @@
 // microseconds (norm, gate, combination, matrix-vector products) with their
 // argument checks, output allocation and current stream in C++.  Through
 // ctypes and Python these cost 10 to 17 us per call, several times the
-// kernel's time for a decoded token; here 4 to 7 us, most of it the launch.
+// kernel's time for a decoded token; here 4 to 6 us, most of it the launch.
 // Each function checks its tensors, allocates the outputs and calls the C
 // ABI of include/fpq.h on the current stream of the tensors' device.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -56,8 +57,10 @@ void* addr(const OptTensor& t) { return t ? t->data_ptr() : nullptr; }
 template <typename T> T* as(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 template <typename T> T* as(const OptTensor& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 
+// For what the kernels write in full: without the dispatcher, half the time
+// of at::empty.
 Tensor empty(const Tensor& like, at::IntArrayRef shape, at::ScalarType type) {
-    return at::empty(shape, like.options().dtype(type));
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 int32_t out_type(at::ScalarType t) {
@@ -213,7 +216,7 @@ py::tuple moe_combine_backward(const Tensor& dout, const Tensor& y, const Tensor
     need(!dy_buffer || is(*dy_buffer, y.scalar_type(), y.sizes()), "need dy of y's type and shape");
     const int32_t type = out_type(y.scalar_type()), d_type = out_type(dout.scalar_type());
     Call call(y, {&dout, &weights, ptr(rows), ptr(dy_buffer)});
-    Tensor dy = dy_buffer ? *dy_buffer : empty(y, y.sizes(), y.scalar_type());
+    Tensor dy = dy_buffer ? *dy_buffer : at::empty(y.sizes(), y.options());
     Tensor dweights = empty(y, weights.sizes(), at::kFloat);
     check(fpq_moe_combine_backward(dout.data_ptr(), d_type, y.data_ptr(), type, y_rows, as<int32_t>(rows),
                                    as<float>(weights), tokens, (int32_t)weights.size(1), hidden, dy.data_ptr(),
