@@ -31,17 +31,20 @@
 // where it is too large.  WK and WR follow from n, k and the form alone, so
 // a row's result does not depend on what else is in the call.
 //
-// Measured (weights of HBM, none in L2): one row x 32768 x 7168 29 us (4.5
-// TB/s), 8 rows 36, 16 rows 51; 8 tokens x 8 of 64 experts, 2048 x 7168, 85
-// us; 2048 x 7168, one row 5.3.  One row is bound by the instructions of the
-// decoding; more rows also by their reads of x from shared memory (as wide
-// as the decoded weights, for every eight columns: without the reads of the
-// second eight 35 us for 16 rows) and its conversion (8 us of those 51).
-// Slower, and not here: the blocks through a ring in shared memory, by
-// asynchronous copies (45 us instead of 37: more instructions) or by TMA and
-// a warp of its own (34.5, 16 rows 48, but 8.7 instead of 5.3 and 100
-// instead of 85 us); two row tiles per warp, which halves the reads of x
-// (16 rows 55: registers).
+// Measured (weights of HBM, none in L2): one row x 32768 x 7168 29 us (4.6
+// TB/s), 8 rows 35.5, 16 rows 45; 2048 x 7168, one row 5.2; 8 tokens x 8 of
+// 64 experts, 2048 x 7168, 83 us, 32 tokens 159.  Bound by the data pipe of
+// the L1 (70% busy for 8 tokens, 80 for 16 rows): a load of codes takes a
+// cycle for each of the eight rows that it touches, and x is read from
+// shared memory in the width of the decoded weights for every eight columns.
+// Its conversion is another 8 us of the 45.  Not better, and not here: loads
+// of 32 bytes, half as many for the pipe (8 tokens 82 us, but 16 rows 48 and
+// one 31: fewer, larger pieces on their way); 24 or 32 warps of fewer
+// registers (16 rows 49 and 59, 8 tokens 88 and 92); the blocks through a
+// ring in shared memory, by asynchronous copies (45 instead of 37 for one
+// row: more instructions) or by TMA and a warp of its own (34.5, 16 rows 48,
+// but 8.7 instead of 5.3 and 100 instead of 85); two row tiles per warp,
+// which halves the reads of x (16 rows 55: registers).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -131,14 +134,16 @@ struct Block {                             // a lane's 32 codes and two scales o
     uint32_t s[2];
 };
 
-// TILES: column tiles of eight (rows of x); CTAS: CTAs per SM.
-template <int TILES, int CTAS>
+// TILES: column tiles of eight (rows of x); CTAS: CTAs per SM; EXPERTS: ids
+// are given.
+template <int TILES, int CTAS, bool EXPERTS>
 __global__ void __launch_bounds__(32 * kGemvWarps / CTAS, CTAS)
 gemv_nvfp4_kernel(const GemvArgs a) {
     constexpr int COLS = 8 * TILES;
     extern __shared__ __align__(16) uint8_t smem[];         // per column a chunk of x, then the blocks' factors
     __shared__ float red[kGemvWarps / CTAS][32][COLS / 2];
-    __shared__ int member[COLS], xrow[COLS], info[2];       // info: members, occurrences before this pair
+    __shared__ int member[COLS], xrow[COLS];
+    __shared__ uint32_t same[32];                            // of each 32 pairs, those of this CTA's expert
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -146,10 +151,16 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     const int64_t tile0 = (int64_t)blockIdx.x * WR;          // the CTA's first 16-row tile
     int64_t e = 0;
     int count;
-    if (a.ids) {
+    if (EXPERTS) {
         // blockIdx.y is a pair; every cap-th pair of an expert takes itself and
-        // the next cap - 1, the others have nothing to do
-        const int p = blockIdx.y, id = a.ids[p];
+        // the next cap - 1, the others have nothing to do and find that out
+        // in one latency of memory: all parts of ids are loaded at once (one
+        // part after the other: 181 us instead of 159 for 32 tokens x 8)
+        const int p = blockIdx.y, id = a.ids[p], parts = (a.m + 31) / 32;
+        for (int c = warp; c < parts; c += threads / 32) {   // whole warps
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, c * 32 + lane < a.m && a.ids[min(c * 32 + lane, a.m - 1)] == id);
+            if (lane == 0) same[c] = mask;
+        }
         e = id;
         if (id < 0 || id >= a.experts) {
             if (tid == 0) raise_device_error(a.err, FPQ_ERR_DEVICE_BAD_INPUT);
@@ -157,31 +168,27 @@ gemv_nvfp4_kernel(const GemvArgs a) {
                 if (tile0 * 16 + i < a.n) put(a.y, (int64_t)p * a.n + tile0 * 16 + i, 0.0f, a.y_f32);
             return;
         }
-        // the CTA's first warp counts the earlier pairs, the last one lists the
-        // later ones (one warp does both if it is alone)
-        if (warp == threads / 32 - 1) {
-            int found = 0;
-            for (int q = p; q < a.m && found < a.cap; q += 32) {
-                const bool same = q + lane < a.m && a.ids[q + lane] == id;
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, same);
-                const int at = found + __popc(mask & ((1u << lane) - 1u));
-                if (same && at < a.cap) {
-                    member[at] = q + lane;
-                    xrow[at] = (q + lane) / a.x_div;
-                }
-                found += __popc(mask);
-            }
-            if (lane == 0) info[0] = min(found, a.cap);
-        }
-        if (warp == 0) {
-            int before = 0;
-            for (int q = 0; q < p; q += 32)
-                before += __popc(__ballot_sync(0xFFFFFFFFu, q + lane < p && a.ids[q + lane] == id));
-            if (lane == 0) info[1] = before;
-        }
         __syncthreads();
-        if (info[1] % a.cap) return;
-        count = info[0];
+        // every warp counts the pairs of the expert before this one, the first
+        // lists it and the next ones; lane c has part c
+        const uint32_t mask = lane < parts ? same[lane] : 0u;
+        const uint32_t earlier = lane < (p >> 5) ? mask : lane == (p >> 5) ? mask & ((1u << (p & 31)) - 1u) : 0u;
+        if (__reduce_add_sync(0xFFFFFFFFu, (unsigned)__popc(earlier)) % (unsigned)a.cap) return;
+        uint32_t later = mask & ~earlier;
+        int at = __popc(later);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, at, o);
+            if (lane >= o) at += u;
+        }
+        count = min(__shfl_sync(0xFFFFFFFFu, at, 31), a.cap);
+        at -= __popc(later);
+        if (warp == 0)
+            for (; later && at < count; later &= later - 1, ++at) {
+                member[at] = lane * 32 + __ffs(later) - 1;
+                xrow[at] = member[at] / a.x_div;
+            }
+        __syncthreads();
     } else {
         count = a.m;
         if (tid < COLS) member[tid] = xrow[tid] = tid;
@@ -334,21 +341,21 @@ gemv_nvfp4_kernel(const GemvArgs a) {
     }
 }
 
-template <int TILES, int CTAS>
+template <int TILES, int CTAS, bool EXPERTS>
 cudaError_t gemv(GemvArgs a, cudaStream_t st) {
     const int groups = (a.k + kGroup * kBlock - 1) / (kGroup * kBlock);
-    a.cols = a.ids ? a.cap : a.m;
+    a.cols = EXPERTS ? a.cap : a.m;
     const int fit = kXBytes / CTAS / (a.cols * kGroup * 256);
     a.chunk = fit < groups ? fit : groups;
     const int blocks = a.chunk * kGroup;
     const int smem = a.cols * (blocks * 256 + 64) + blocks * 8 * TILES * (int)sizeof(float);
-    const auto kernel = gemv_nvfp4_kernel<TILES, CTAS>;
+    const auto kernel = gemv_nvfp4_kernel<TILES, CTAS, EXPERTS>;
     if (smem > 32 * 1024) {                                  // with the static arrays, past what needs no opt-in
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     const int64_t tiles = (a.n + 15) / 16;
-    return launch_pdl(kernel, dim3((unsigned)((tiles + a.wr - 1) / a.wr), (unsigned)(a.ids ? a.m : 1)),
+    return launch_pdl(kernel, dim3((unsigned)((tiles + a.wr - 1) / a.wr), (unsigned)(EXPERTS ? a.m : 1)),
                       dim3(32u * a.wk * a.wr), smem, st, a);
 }
 
@@ -358,7 +365,7 @@ cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, c
                               const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
                               int y_f32, uint32_t* err, int sms, cudaStream_t st) {
     // As many warps along k as leave one wave of an SM's sixteen, up to one for
-    // each group (2048 x 7168, one row: 16 warps for 14 groups 5.3 us, 8 warps
+    // each group (2048 x 7168, one row: 16 warps for 14 groups 5.2 us, 8 warps
     // 6.8), then as many row tiles per CTA as bring the CTAs into one
     // wave: with 148 SMs and two CTAs each, 2048 tiles become 293 CTAs of
     // seven warps; 128 tiles become 128 CTAs of sixteen.  The expert form
@@ -378,7 +385,8 @@ cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, c
     const int cap = wide ? 16 : tokens < 4 ? tokens : m <= 2 * (int64_t)experts ? 4 : 8;
     const GemvArgs a{(const uint16_t*)x, (int)m, x_div, ids, experts, (const uint8_t*)wq, (const uint8_t*)ws, wg, n,
                      (int)k, y, err, y_f32, cap, wk, (int)wr, 0, 0};
-    return wide ? gemv<2, 1>(a, st) : ctas == 1 ? gemv<1, 1>(a, st) : gemv<1, 2>(a, st);
+    if (ids) return wide ? gemv<2, 1, true>(a, st) : ctas == 1 ? gemv<1, 1, true>(a, st) : gemv<1, 2, true>(a, st);
+    return wide ? gemv<2, 1, false>(a, st) : ctas == 1 ? gemv<1, 1, false>(a, st) : gemv<1, 2, false>(a, st);
 }
 
 }  // namespace fpq
