@@ -378,24 +378,29 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     if (!a.partial) return;
     float4* out = reinterpret_cast<float4*>(a.partial) + (int64_t)blockIdx.x * a.nvec * 2;
     if (WARP) {
-        // the CTA's eight warps add their sums in order, in the rings' place
-        float* acc_s = reinterpret_cast<float*>(smem);
-        for (int wi = 0; wi < kRowWarps; ++wi) {
-            __syncthreads();
-            if (team == wi) {
+        // the warps' sums side by side in the rings' place (a ring has at least
+        // 96 bytes per vector, they take 32), then added in the warps' order
+        float4* const sums = reinterpret_cast<float4*>(smem);
+        __syncthreads();
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (t + i * T < a.nvec)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float* p = &acc_s[(t + i * T) * 8 + j];
-                            const float u = j & 1 ? hi_of(acc[i][j / 2]) : lo_of(acc[i][j / 2]);
-                            *p = wi ? *p + u : u;
-                        }
+        for (int i = 0; i < V; ++i) {
+            const int v = t + i * T;
+            if (v < a.nvec) {
+                float4* p = sums + (team * a.nvec + v) * 2;
+                p[0] = make_float4(lo_of(acc[i][0]), hi_of(acc[i][0]), lo_of(acc[i][1]), hi_of(acc[i][1]));
+                p[1] = make_float4(lo_of(acc[i][2]), hi_of(acc[i][2]), lo_of(acc[i][3]), hi_of(acc[i][3]));
             }
         }
         __syncthreads();
-        for (int v = threadIdx.x; v < 2 * a.nvec; v += blockDim.x) out[v] = reinterpret_cast<float4*>(acc_s)[v];
+        for (int v = threadIdx.x; v < 2 * a.nvec; v += blockDim.x) {
+            float4 s = sums[v];
+#pragma unroll
+            for (int wi = 1; wi < kRowWarps; ++wi) {
+                const float4 u = sums[wi * 2 * a.nvec + v];
+                s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
+            }
+            out[v] = s;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -549,7 +554,6 @@ BwdPlan bwd_plan(int nvec) {
     p.stages = (kBwdSmem / p.ctas - w) / stage;
     if (p.stages > kBwdMaxStages) p.stages = kBwdMaxStages;
     p.smem = w + p.stages * stage;
-    if (warp && p.smem < nvec * 32) p.smem = nvec * 32;      // the warps' sums
     return p;
 }
 
