@@ -247,19 +247,20 @@ struct NormBwdArgs {
     uint32_t* err;
 };
 
+constexpr int kBwdMaxWarps = 16;          // rows (warps) per CTA in the warp-per-row form
 constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 216 * 1024;        // rings of the CTAs of an SM
 
 // A team (the CTA, or a warp) takes batches of consecutive rows, every
 // grid-th; a thread's columns are the same for every row.
 template <int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 512)
+__global__ void __launch_bounds__(512, 1)
 rmsnorm_bwd_kernel(const NormBwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];         // w, then the rings: stages of dy, x, dres rows
-    __shared__ uint64_t bars[WARP ? kRowWarps : 1][kBwdMaxStages];
+    __shared__ uint64_t bars[WARP ? kBwdMaxWarps : 1][kBwdMaxStages];
     __shared__ float red[2][32];
     const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, T = WARP ? 32 : blockDim.x;
-    const int team = WARP ? threadIdx.x >> 5 : 0;
+    const int team = WARP ? threadIdx.x >> 5 : 0, cta_teams = WARP ? blockDim.x >> 5 : 1;
     const uint32_t row_bytes = (uint32_t)a.nvec * 16, part = row_bytes * a.batch;
     uint4* const wsm = reinterpret_cast<uint4*>(smem);
     uint8_t* const ring = smem + (row_bytes + 127) / 128 * 128 + team * a.stages * 3 * part;
@@ -273,8 +274,7 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) wsm[v] = __ldg(a.w + v);
     __syncthreads();
 
-    const int64_t teams = WARP ? (int64_t)gridDim.x * kRowWarps : gridDim.x;
-    const int64_t first = WARP ? (int64_t)blockIdx.x * kRowWarps + team : blockIdx.x;
+    const int64_t teams = (int64_t)gridDim.x * cta_teams, first = (int64_t)blockIdx.x * cta_teams + team;
     const int64_t batches = (a.rows + a.batch - 1) / a.batch;
     const auto fill = [&](int64_t b, int stage) {            // one thread of the team
         if (b >= batches) return;
@@ -394,8 +394,8 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
         __syncthreads();
         for (int v = threadIdx.x; v < 2 * a.nvec; v += blockDim.x) {
             float4 s = sums[v];
-#pragma unroll
-            for (int wi = 1; wi < kRowWarps; ++wi) {
+#pragma unroll 4
+            for (int wi = 1; wi < cta_teams; ++wi) {
                 const float4 u = sums[wi * 2 * a.nvec + v];
                 s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
             }
@@ -538,19 +538,23 @@ struct BwdPlan {
 constexpr int kRingVectors = kBwdSmem / 16 / 7 / 128 * 128;
 static_assert(kRingVectors * 16 + 2 * 3 * kRingVectors * 16 <= kBwdSmem, "a ring has two stages");
 
-BwdPlan bwd_plan(int nvec) {
+BwdPlan bwd_plan(int64_t rows, int nvec, int sms) {
     BwdPlan p{};
     const bool warp = nvec <= 128;
     p.v = warp ? (nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4) : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
-    p.threads = warp ? 32 * kRowWarps : ((nvec + p.v - 1) / p.v + 31) / 32 * 32;
     // short rows are copied several at a time, 2 KB per operand
     p.batch = warp ? 128 / nvec : 1;
+    // Sixteen warps hide each other's latency where there are rows for them
+    // (16384 x 1024 27.6 us, eight warps 30.3); few rows are spread over more
+    // CTAs (300 x 1024 5.2 us, sixteen warps 6.0).
+    const int warps = (rows + p.batch - 1) / p.batch > 8 * (int64_t)sms ? kBwdMaxWarps : kBwdMaxWarps / 2;
+    p.threads = warp ? 32 * warps : ((nvec + p.v - 1) / p.v + 31) / 32 * 32;
     // About 512 threads per SM: with 8192 x 7168 (448 threads) one CTA of four
     // stages takes 78 us and two of two stages 85 us, with 16384 x 2048 (128
     // threads) two CTAs 74 us and four 65 us.
     p.ctas = warp ? 1 : 512 / p.threads > 4 ? 4 : 512 / p.threads;
     if (nvec > kRingVectors) return p;
-    const int row = nvec * 16, stage = 3 * row * p.batch * (warp ? kRowWarps : 1), w = (row + 127) / 128 * 128;
+    const int row = nvec * 16, stage = 3 * row * p.batch * (warp ? warps : 1), w = (row + 127) / 128 * 128;
     p.stages = (kBwdSmem / p.ctas - w) / stage;
     if (p.stages > kBwdMaxStages) p.stages = kBwdMaxStages;
     p.smem = w + p.stages * stage;
@@ -558,7 +562,8 @@ BwdPlan bwd_plan(int nvec) {
 }
 
 int bwd_grid(int64_t rows, const BwdPlan& p, int nvec, int sms) {
-    const int64_t tasks = nvec <= 128 ? ((rows + p.batch - 1) / p.batch + kRowWarps - 1) / kRowWarps : rows;
+    const int warps = p.threads / 32;
+    const int64_t tasks = nvec <= 128 ? ((rows + p.batch - 1) / p.batch + warps - 1) / warps : rows;
     return (int)min64(tasks, (int64_t)sms * p.ctas);
 }
 
@@ -583,14 +588,14 @@ cudaError_t launch_rmsnorm_quantize(int fmt, const void* x, int64_t ld_x, const 
 
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, int sms) {
     const int nvec = (int)(cols / 8);
-    return (size_t)bwd_grid(rows, bwd_plan(nvec), nvec, sms) * (size_t)cols * sizeof(float);
+    return (size_t)bwd_grid(rows, bwd_plan(rows, nvec, sms), nvec, sms) * (size_t)cols * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x, const void* weight,
                                     const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
                                     float* dweight, void* workspace, uint32_t* err, int sms, cudaStream_t st) {
     const int nvec = (int)(cols / 8);
-    const BwdPlan p = bwd_plan(nvec);
+    const BwdPlan p = bwd_plan(rows, nvec, sms);
     const int grid = bwd_grid(rows, p, nvec, sms);
     const NormBwdArgs a{(const uint8_t*)dy, (const uint8_t*)x, ld_x * 2, (const uint4*)weight, rstd,
                         (const uint8_t*)dres, rows, nvec, (float)cols, (uint4*)dx,
