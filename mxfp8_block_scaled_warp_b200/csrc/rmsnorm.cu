@@ -252,13 +252,14 @@ constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 216 * 1024;        // rings of the CTAs of an SM
 
 // A team (the CTA, or a warp) takes batches of consecutive rows, every
-// grid-th; a thread's columns are the same for every row.
-template <int V, bool WARP>
+// grid-th; a thread's columns are the same for every row.  WREG: its weights
+// stay in registers too.
+template <int V, bool WARP, bool WREG>
 __global__ void __launch_bounds__(512, 1)
 rmsnorm_bwd_kernel(const NormBwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];         // w, then the rings: stages of dy, x, dres rows
     __shared__ uint64_t bars[WARP ? kBwdMaxWarps : 1][kBwdMaxStages];
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
     const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, T = WARP ? 32 : blockDim.x;
     const int team = WARP ? threadIdx.x >> 5 : 0, cta_teams = WARP ? blockDim.x >> 5 : 1;
     const uint32_t row_bytes = (uint32_t)a.nvec * 16, part = row_bytes * a.batch;
@@ -266,6 +267,7 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     uint8_t* const ring = smem + (row_bytes + 127) / 128 * 128 + team * a.stages * 3 * part;
     uint64_t* const bar = bars[team];
     pdl_trigger();
+    if (WREG && t < 32) red[0][t] = red[1][t] = 0.0f;        // slots past the last warp stay 0
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
         sm100::fence_barrier_init();
@@ -297,6 +299,11 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     // KEEP: the row stays in registers between the two passes, so that its
     // stage is refilled between them; rows too long for that are read twice
     constexpr bool KEEP = V <= 2;
+    static_assert(KEEP || !WREG, "the second pass reads the weights from shared memory");
+    uint64_t wr[WREG ? V : 1][4];
+    if (WREG)
+#pragma unroll
+        for (int i = 0; i < V; ++i) unpack4(t + i * T < a.nvec ? wsm[t + i * T] : make_uint4(0, 0, 0, 0), wr[WREG ? i : 0]);
     uint64_t acc[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -331,7 +338,12 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
                 uint64_t d[4], w[4];
                 unpack4(dv[v], d);
                 unpack4(xv[v], x[k]);
-                unpack4(wsm[v], w);
+                if (WREG) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = wr[WREG ? i : 0][j];
+                } else {
+                    unpack4(wsm[v], w);
+                }
                 if (KEEP && a.dres) e[k] = ev[v];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -340,7 +352,20 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
                     acc[i][j] = fma2(d[j], mul2(x[k][j], rstd2), acc[i][j]);
                 }
             }
-            const float dot = row_sum<WARP>(lo_of(dot2) + hi_of(dot2), red[turn]);
+            float dot;
+            if (WREG) {
+                // every thread adds the warps' sums itself: one latency, where a
+                // second round of shuffles has five (8192 x 7168: 0.4 us)
+                dot = warp_sum(lo_of(dot2) + hi_of(dot2));
+                if ((t & 31) == 0) red[turn][t >> 5] = dot;
+                __syncthreads();
+                const float4* r = reinterpret_cast<const float4*>(red[turn]);
+                const float4 s0 = r[0], s1 = r[1], s2 = r[2], s3 = r[3];
+                dot = (((s0.x + s0.y) + (s0.z + s0.w)) + ((s1.x + s1.y) + (s1.z + s1.w))) +
+                      (((s2.x + s2.y) + (s2.z + s2.w)) + ((s3.x + s3.y) + (s3.z + s3.w)));
+            } else {
+                dot = row_sum<WARP>(lo_of(dot2) + hi_of(dot2), red[turn]);
+            }
             if (!WARP && t == 0) {
                 // every thread of the CTA is past its reads of this row (KEEP)
                 // or has left the previous one
@@ -567,9 +592,9 @@ int bwd_grid(int64_t rows, const BwdPlan& p, int nvec, int sms) {
     return (int)min64(tasks, (int64_t)sms * p.ctas);
 }
 
-template <int V, bool WARP>
+template <int V, bool WARP, bool WREG = false>
 cudaError_t launch_bwd(const NormBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t st) {
-    const auto kernel = rmsnorm_bwd_kernel<V, WARP>;
+    const auto kernel = rmsnorm_bwd_kernel<V, WARP, WREG>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3((unsigned)p.threads), p.smem, st, a);
@@ -606,6 +631,10 @@ cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x,
         if (nvec <= 32) e = launch_bwd<1, true>(a, p, grid, st);
         else if (nvec <= 64) e = launch_bwd<2, true>(a, p, grid, st);
         else if (nvec <= 128) e = launch_bwd<4, true>(a, p, grid, st);
+        // 8192 x 7168 77.9 us with the weights in registers, 80.6 without; with
+        // several CTAs per SM they cost more than they save (16384 x 2048 66
+        // us with, 47.8 without)
+        else if (nvec <= 1024 && p.ctas == 1) e = launch_bwd<2, false, true>(a, p, grid, st);
         else if (nvec <= 1024) e = launch_bwd<2, false>(a, p, grid, st);
         else if (nvec <= kRingVectors) e = launch_bwd<4, false>(a, p, grid, st);
         else if (nvec <= 2048) e = launch_pdl(rmsnorm_bwd_long_kernel<4>, g, b, 0, st, a);
