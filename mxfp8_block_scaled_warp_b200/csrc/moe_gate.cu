@@ -28,12 +28,15 @@
 // the other: the topk-th largest of the 32 lane maxima bounds them from
 // below, the few keys at or above it (ten for eight of 256) are gathered, one
 // per lane, and each counts how many are before it, which is its place in
-// the output.  (Taking one maximum after the other: 51 us for 16384 tokens,
-// 256 experts in groups; it remains for rows with more than 32 such keys,
-// which take equal logits.)  Measured for eight of 256, 16384 tokens, fp32:
-// 12.5 us without a bias (1.4 TB/s), sigmoid with one 18.6, in eight groups
-// 26.7 (at 70% of the issue slots), softmax with a bias 27.4; 16 tokens in
-// groups 5.3 us, which is one warp's latency.
+// the output.  The bound itself and the choice of groups are counted too, not
+// taken one maximum after the other: for a few tokens the kernel is the
+// latency of one warp's steps (16 tokens of 256 experts in groups 3.8 us
+// instead of 5.4).  One maximum after the other remains for rows with more
+// than 32 such keys, which take equal logits, and for groups too near to
+// tell; throughout it took 51 us for 16384 tokens.  Measured for eight of 256,
+// 16384 tokens, fp32: 13.0 us without a bias (1.4 TB/s), sigmoid with one
+// 18.4, in eight groups 27.4 (at 70% of the issue slots), softmax with a bias
+// 26.4.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_kernel(const GateArgs a) {
     extern __shared__ float sh[];                           // per warp: keys of the row, padded per 32 (groups only)
     __shared__ uint2 gathered[kGateWarps][32];               // key pattern, expert
+    __shared__ uint4 tops[kGateWarps][8];                    // the lanes' largest keys
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
@@ -136,6 +140,9 @@ moe_gate_kernel(const GateArgs a) {
     float l[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) l[i] = 32 * i + lane < E ? load_logit<T>(row + 32 * i + lane) : -INFINITY;
+    float b[VPT];                                            // loaded with the logits: one latency
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) b[i] = a.bias && 32 * i + lane < E ? __ldg(a.bias + 32 * i + lane) : 0.0f;
 
     // softmax maximum and sum, where the scores themselves are needed (the
     // weights take the sum only without renormalize)
@@ -186,7 +193,7 @@ moe_gate_kernel(const GateArgs a) {
         float k = l[i];
         if (scores && e < E) {
             float r = score_key(l[i]);
-            if (a.bias) r += __ldg(a.bias + e);
+            if (a.bias) r += b[i];
             if (a.bias && l[i] != -INFINITY) k = r;          // a masked expert gains nothing by its bias
             if (a.n_group > 1) s[e + i] = r == r ? r : -INFINITY;
         }
@@ -214,8 +221,22 @@ moe_gate_kernel(const GateArgs a) {
         const float rank = a.group_top == 2 ? first + second : first;
         const bool holds = g < a.n_group && (lane & (split - 1)) == 0;
         uint32_t gkey = holds ? pattern(rank) : kTaken;
-        uint32_t open = 0;                                   // chosen groups
-        for (int c = 0; c < a.topk_group; ++c) {
+        // each group counts the ranks above its own; only where two are too
+        // near to tell are the best taken one after the other
+        const float own = value(gkey), reach = slack(own, a.group_top);
+        int above = 0;
+        bool close = false;
+#pragma unroll 4
+        for (int j = 0; j < a.n_group; ++j) {
+            const int holder = j << shift;
+            const uint32_t k = __shfl_sync(kFull, gkey, holder);
+            above += k > gkey || (k == gkey && holder < lane);
+            close |= holder != lane && k > kNaN && gkey > kNaN && (k == gkey || fabsf(value(k) - own) <= reach);
+        }
+        const bool apart = !__any_sync(kFull, holds && close);
+        uint32_t open = __ballot_sync(kFull, holds && above < a.topk_group);   // lanes of the chosen groups
+        if (!apart) open = 0;
+        for (int c = apart ? a.topk_group : 0; c < a.topk_group; ++c) {
             const uint32_t m = __reduce_max_sync(kFull, gkey);
             const float least = value(m) - slack(value(m), a.group_top);
             const bool near = gkey != kTaken && (gkey == m || (gkey > kNaN && value(gkey) >= least));
@@ -246,7 +267,7 @@ moe_gate_kernel(const GateArgs a) {
                     if (best < 0 || r > most) { best = holder; most = r; }   // equal ones: the lowest group
                 }
             }
-            open |= 1u << (best >> shift);
+            open |= 1u << best;
             if (lane == best) gkey = kTaken;
         }
         // e / size for e < 1024: the reciprocal is off by less than e / 2^20 < 1 / size
@@ -254,7 +275,7 @@ moe_gate_kernel(const GateArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = 32 * i + lane;
-            if (e < E && !((open >> ((e * inverse) >> 20)) & 1u)) key[i] = kOutside;
+            if (e < E && !((open >> (((e * inverse) >> 20) << shift)) & 1u)) key[i] = kOutside;
         }
     }
 
@@ -262,14 +283,15 @@ moe_gate_kernel(const GateArgs a) {
     uint32_t top = key[0];
 #pragma unroll
     for (int i = 1; i < VPT; ++i) top = max(top, key[i]);
-    uint32_t bound = 0;
-    for (int have = 0; have < a.topk;) {
-        bound = __reduce_max_sync(kFull, top);
-        const uint32_t equal = __ballot_sync(kFull, top == bound);
-        have += __popc(equal);
-        if (bound == kTaken) break;
-        if (top == bound) top = kTaken;
+    reinterpret_cast<uint32_t*>(tops[warp])[lane] = top;
+    __syncwarp();
+    int from = 0;                                            // lanes whose largest is not below this one's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 u = tops[warp][i];
+        from += (u.x >= top) + (u.y >= top) + (u.z >= top) + (u.w >= top);
     }
+    uint32_t bound = __reduce_max_sync(kFull, from >= a.topk ? top : 0u);
     if (a.bias && bound > kNaN) bound = pattern(value(bound) - slack(value(bound), 1));
     bound = max(bound, kNaN);                                // there are topk experts inside the chosen groups
     int count = 0;
@@ -292,6 +314,7 @@ moe_gate_kernel(const GateArgs a) {
         bool near = false;
         if (a.bias) {
             const float v = value(c.x), reach = slack(v, 1);
+#pragma unroll 4
             for (int j = 0; j < count; ++j) {
                 const uint32_t k = __shfl_sync(kFull, c.x, j);
                 place += (k > c.x || (k == c.x && j < lane)) ? 1 : 0;
