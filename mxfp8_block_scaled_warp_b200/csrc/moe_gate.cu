@@ -37,6 +37,8 @@
 // 16384 tokens, fp32: 13.0 us without a bias (1.4 TB/s), sigmoid with one
 // 18.4, in eight groups 27.4 (at 70% of the issue slots), softmax with a bias
 // 26.4.
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -612,50 +614,73 @@ moe_gate_bwd_kernel(const GateBwdArgs a) {
     if (first) put(id, g);
 }
 
-// The softmax over all experts: a warp per token, its row assembled in shared
-// memory (16384 x 256 fp32: 13.6 us, 2.5 TB/s; the exponentials bound it).
-template <typename T>
+// The softmax over all experts: a warp per token, the row read once into
+// registers and one exponential per logit; every entry is written as one that
+// was not chosen, then the chosen ones again.  16384 x 256 fp32 8.6 us (3.9
+// TB/s), 8192 x 512 6.6; read three times, with the chosen entries added in
+// shared memory, 13.6 and 14.6.
+template <typename T, int VPT>
 __global__ void __launch_bounds__(32 * kGateWarps)
 moe_gate_bwd_dense_kernel(const GateBwdArgs a) {
-    extern __shared__ __align__(16) float sh[];
     pdl_trigger();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts, K = a.topk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
     const int64_t tok = (int64_t)blockIdx.x * kGateWarps + warp;
     if (tok >= a.tokens) return;
-    float* d = sh + warp * ((E + 3) / 4 * 4);
     const T* row = static_cast<const T*>(a.logits) + tok * E;
-    const int id = checked_id(a, tok, lane, lane < K);
+    float l[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) l[i] = 32 * i + lane < E ? load_logit<T>(row + 32 * i + lane) : -INFINITY;
+    const int id = checked_id(a, tok, lane, lane < a.topk);
     const bool have = id >= 0;
-    const float v = have ? a.scale * a.dweights[tok * K + lane] : 0.0f;
+    const float v = have ? a.scale * a.dweights[tok * a.topk + lane] : 0.0f;
     const float x = have ? load_logit<T>(row + id) : -INFINITY;
-    float mx = -INFINITY, sum = 0.0f;
-    for (int e = lane; e < E; e += 32) {
-        d[e] = 0.0f;
-        mx = fmaxf(mx, load_logit<T>(row + e));
-    }
+    float mx = -INFINITY, sum = 0.0f, inverse = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) mx = fmaxf(mx, l[i]);
     mx = warp_max(mx);
-    if (mx != -INFINITY) {
-        for (int e = lane; e < E; e += 32) sum += expf(load_logit<T>(row + e) - mx);
-        sum = warp_sum(sum);
+    const bool some = mx != -INFINITY;                       // else every score is 0
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        l[i] = some && 32 * i + lane < E ? expf(l[i] - mx) : 0.0f;
+        sum += l[i];
     }
-    const float p = have && mx != -INFINITY ? __fdiv_rn(expf(x - mx), sum) : 0.0f;
-    const float dot = warp_sum(v * p);
-    __syncwarp();
-    // one choice after the other, by the lane that owns the expert: an id
-    // named twice gets the sum, in the order of the choices
-    for (int j = 0; j < K; ++j) {
-        const int e = __shfl_sync(kFull, id, j);
-        const float vj = __shfl_sync(kFull, v, j);
-        if (e >= 0 && (e & 31) == lane) d[e] += vj;
-    }
+    sum = warp_sum(sum);
+    if (some) inverse = __fdiv_rn(1.0f, sum);
+    const float p = have && some ? expf(x - mx) * inverse : 0.0f;
+    const float dot = warp_sum(v * p), other = -dot * inverse;
     T* out = static_cast<T*>(a.dlogits) + tok * E;
-    for (int e = lane; e < E; e += 32) {                     // the lane's own entries
-        const float pe = mx != -INFINITY ? __fdiv_rn(expf(load_logit<T>(row + e) - mx), sum) : 0.0f;
-        const float f = pe * (d[e] - dot);
+    const auto put = [&](int e, float f) {
         if (sizeof(T) == 4) reinterpret_cast<float*>(out)[e] = f;
         else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(f);
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        if (32 * i + lane < E) put(32 * i + lane, l[i] * other);
+    // an id named twice gets the sum, in the order of the choices
+    const uint32_t same = __match_any_sync(kFull, have ? id : -1 - lane);
+    const bool first = have && __ffs(same) - 1 == lane;
+    float mine = v;
+    if (__any_sync(kFull, have && !first)) {
+        mine = 0.0f;
+        for (int j = 0; j < 32; ++j) {
+            const float vj = __shfl_sync(kFull, v, j);
+            if ((same >> j) & 1u) mine += vj;
+        }
     }
+    __syncwarp();                                            // after the others
+    if (first) put(id, p * (mine - dot));
+}
+
+// By the registers that a row of E takes at 32 lanes.
+template <typename F>
+cudaError_t by_registers(int E, F&& f) {
+    if (E <= 32) return f(std::integral_constant<int, 1>());
+    if (E <= 64) return f(std::integral_constant<int, 2>());
+    if (E <= 128) return f(std::integral_constant<int, 4>());
+    if (E <= 256) return f(std::integral_constant<int, 8>());
+    if (E <= 512) return f(std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 32>());
 }
 
 template <typename T, bool SIGMOID>
@@ -676,12 +701,9 @@ cudaError_t gate(const GateArgs& a, cudaStream_t st) {
             return merge(moe_gate_merge_kernel<T, SIGMOID, 32>, 32);
         }
     }
-    if (E <= 32) return launch_pdl(moe_gate_kernel<T, SIGMOID, 1>, grid, block, smem, st, a);
-    if (E <= 64) return launch_pdl(moe_gate_kernel<T, SIGMOID, 2>, grid, block, smem, st, a);
-    if (E <= 128) return launch_pdl(moe_gate_kernel<T, SIGMOID, 4>, grid, block, smem, st, a);
-    if (E <= 256) return launch_pdl(moe_gate_kernel<T, SIGMOID, 8>, grid, block, smem, st, a);
-    if (E <= 512) return launch_pdl(moe_gate_kernel<T, SIGMOID, 16>, grid, block, smem, st, a);
-    return launch_pdl(moe_gate_kernel<T, SIGMOID, 32>, grid, block, smem, st, a);
+    return by_registers(E, [&](auto n) {
+        return launch_pdl(moe_gate_kernel<T, SIGMOID, decltype(n)::value>, grid, block, smem, st, a);
+    });
 }
 
 }  // namespace
@@ -699,23 +721,24 @@ cudaError_t launch_moe_gate_backward(const void* logits, int f32, const int32_t*
                                      int64_t tokens, int experts, int sigmoid, int topk, int renormalize,
                                      float scale, void* dlogits, uint32_t* err, cudaStream_t st) {
     const GateBwdArgs a{logits, ids, dweights, tokens, experts, topk, renormalize, scale, dlogits, err};
-    const auto launch = [&](auto kernel, int per_warp, size_t smem) {
+    const auto launch = [&](auto kernel, int per_warp) {
         const int64_t per = kGateWarps * per_warp;
-        return launch_pdl(kernel, dim3((unsigned)((tokens + per - 1) / per)), dim3(32 * kGateWarps), smem, st, a);
+        return launch_pdl(kernel, dim3((unsigned)((tokens + per - 1) / per)), dim3(32 * kGateWarps), 0, st, a);
     };
-    if (!sigmoid && !renormalize) {
-        const size_t smem = (size_t)kGateWarps * ((experts + 3) / 4 * 4) * sizeof(float);
-        return f32 ? launch(moe_gate_bwd_dense_kernel<float>, 1, smem) : launch(moe_gate_bwd_dense_kernel<uint16_t>, 1, smem);
-    }
+    if (!sigmoid && !renormalize)
+        return by_registers(experts, [&](auto n) {
+            constexpr int VPT = decltype(n)::value;
+            return f32 ? launch(moe_gate_bwd_dense_kernel<float, VPT>, 1) : launch(moe_gate_bwd_dense_kernel<uint16_t, VPT>, 1);
+        });
     // four tokens per warp where their choices fit: a quarter of the instructions
     if (topk <= 8) {
         if (f32)
-            return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 8>, 4, 0) : launch(moe_gate_bwd_kernel<float, false, 8>, 4, 0);
-        return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 8>, 4, 0) : launch(moe_gate_bwd_kernel<uint16_t, false, 8>, 4, 0);
+            return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 8>, 4) : launch(moe_gate_bwd_kernel<float, false, 8>, 4);
+        return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 8>, 4) : launch(moe_gate_bwd_kernel<uint16_t, false, 8>, 4);
     }
     if (f32)
-        return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 32>, 1, 0) : launch(moe_gate_bwd_kernel<float, false, 32>, 1, 0);
-    return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 32>, 1, 0) : launch(moe_gate_bwd_kernel<uint16_t, false, 32>, 1, 0);
+        return sigmoid ? launch(moe_gate_bwd_kernel<float, true, 32>, 1) : launch(moe_gate_bwd_kernel<float, false, 32>, 1);
+    return sigmoid ? launch(moe_gate_bwd_kernel<uint16_t, true, 32>, 1) : launch(moe_gate_bwd_kernel<uint16_t, false, 32>, 1);
 }
 
 }  // namespace fpq

@@ -285,3 +285,21 @@ def test_groups_pass_over_a_nan(fpq):
     lg[1, 2], lg[1, 0] = at(0.9), math.nan                           # before and behind the others
     ids, _ = moe.gate(lg, 2, score=moe.SIGMOID, n_group=2, topk_group=1, group_top=2)
     assert torch.equal(ids.cpu(), torch.tensor([[4, 5], [4, 5]], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("experts", [7, 64, 200, 1024])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_backward_of_the_full_softmax_with_an_id_named_twice(fpq, experts, dtype):
+    lg = _logits(9, experts, experts, dtype)
+    ids = torch.randint(0, experts, (9, 6), generator=torch.Generator().manual_seed(3)).int().cuda()
+    ids[:, 3] = ids[:, 1]
+    ids[4] = ids[4, 0]
+    dw = torch.randn((9, 6), generator=torch.Generator().manual_seed(4)).cuda()
+    d = moe.gate_backward(dw, lg, ids, renormalize=False, scale=0.5)
+    p = _scores(lg.double(), moe.SOFTMAX)
+    v = 0.5 * dw.double()
+    dot = (v * p.gather(1, ids.long())).sum(1, keepdim=True)
+    want = p * (torch.zeros_like(p).scatter_add_(1, ids.long(), v) - dot)
+    size = p * (v.abs().sum(1, keepdim=True))
+    rel = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    assert torch.all((d.double() - want).abs() <= rel * want.abs() + 2.0 ** -15 * size + 1e-37)
