@@ -266,7 +266,6 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     uint4* const wsm = reinterpret_cast<uint4*>(smem);
     uint8_t* const ring = smem + (row_bytes + 127) / 128 * 128 + team * a.stages * 3 * part;
     uint64_t* const bar = bars[team];
-    pdl_trigger();
     if (WREG && t < 32) red[0][t] = red[1][t] = 0.0f;        // slots past the last warp stay 0
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
@@ -400,6 +399,11 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
         }
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
     }
+    // Only now: CTAs of the next kernel on this one's SMs, and of the next
+    // call's beside those, would keep some of a wave's CTAs waiting for a
+    // whole wave (16384 x 2048, call after call: 68 us instead of 47).  For
+    // the same reason the kernel that adds the sums triggers by its end.
+    pdl_trigger();
     if (!a.partial) return;
     float4* out = reinterpret_cast<float4*>(a.partial) + (int64_t)blockIdx.x * a.nvec * 2;
     if (WARP) {
@@ -445,7 +449,6 @@ template <int V>
 __global__ void __launch_bounds__(512)
 rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
     __shared__ float red[2][32];
-    pdl_trigger();
     pdl_wait();
     const int t = threadIdx.x, T = blockDim.x;
     uint64_t acc[V][4];
@@ -510,6 +513,7 @@ rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
             }
         }
     }
+    pdl_trigger();
     if (!a.partial) return;
     float4* out = reinterpret_cast<float4*>(a.partial) + (int64_t)blockIdx.x * a.nvec * 2;
 #pragma unroll
@@ -522,17 +526,30 @@ rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
     }
 }
 
-// dweight[c] = sum of the partial rows, in a fixed order: a CTA takes 32
-// columns; thread (i, j) adds rows i, i + 32, ... of its four, then the
-// threads of a column are added in order.
-constexpr int kSumRows = 32, kSumVecs = 8;
+// dweight[c] = sum of the partial rows, in a fixed order: a CTA takes 16
+// columns; thread (i, j) adds rows i, i + 128, ... of its four, all loads in
+// flight at once (there are at most four rows per SM), then the threads of a
+// column are added, in a warp and across the warps.  Latency alone, about 3
+// us of the call (4 us with 32 rows of threads).
+constexpr int kSumRows = 128, kSumVecs = 4, kSumWarps = kSumRows * kSumVecs / 32;
+
+__device__ __forceinline__ float4 sum_rows(float4 s) {       // over the lanes of a vector
+#pragma unroll
+    for (int o = kSumVecs; o < 32; o <<= 1) {
+        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+        s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
+        s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, o);
+    }
+    return s;
+}
 
 __global__ void __launch_bounds__(kSumRows * kSumVecs)
 rmsnorm_dweight_kernel(const float4* __restrict__ partial, int parts, int nvec4, float4* __restrict__ dweight) {
-    __shared__ float4 sum[kSumRows][kSumVecs];
-    pdl_trigger();
+    __shared__ float4 sum[kSumWarps][kSumVecs];
     pdl_wait();
     const int i = threadIdx.x / kSumVecs, j = threadIdx.x % kSumVecs, v = blockIdx.x * kSumVecs + j;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (v < nvec4) {
 #pragma unroll 8
@@ -541,15 +558,15 @@ rmsnorm_dweight_kernel(const float4* __restrict__ partial, int parts, int nvec4,
             s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
         }
     }
-    sum[i][j] = s;
+    s = sum_rows(s);
+    if (lane < kSumVecs) sum[warp][lane] = s;
     __syncthreads();
-    if (i == 0 && v < nvec4) {
-#pragma unroll
-        for (int r = 1; r < kSumRows; ++r) {
-            const float4 u = sum[r][j];
-            s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
-        }
-        dweight[v] = s;
+    if (warp == 0) {
+        // lane (w, j) adds warps w and w + 8
+        static_assert(kSumWarps == 16 && kSumVecs == 4, "two warps' sums per lane");
+        const float4 c = sum[lane >> 2][j], d = sum[(lane >> 2) + 8][j];
+        s = sum_rows(make_float4(c.x + d.x, c.y + d.y, c.z + d.z, c.w + d.w));
+        if (lane < kSumVecs && v < nvec4) dweight[v] = s;
     }
 }
 
