@@ -24,9 +24,10 @@
 // into registers 101).
 //
 // Measured at 8192 x 7168: residual, bf16 and MXFP8 out 81 us (6.53 TB/s, the
-// rate of a copy), FP8 without bf16 68 us; backward with dres 78 us (5.98
-// TB/s; what is left is the few CTAs' waits between a row's two passes).  A
-// row of 7168 2.3 us.
+// rate of a copy), FP8 without bf16 68 us; backward with dres 77.5 us (6.06
+// TB/s), 3 to 4 of them the second kernel's; without dres, a quarter less to
+// move, 74.3: a row's two passes set the pace.  16384 x 1024 backward 26.4 us
+// (5.1 TB/s).  A row of 7168 2.3 us, backward 5.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -252,9 +253,8 @@ constexpr int kBwdMaxStages = 4;
 constexpr int kBwdSmem = 216 * 1024;        // rings of the CTAs of an SM
 
 // A team (the CTA, or a warp) takes batches of consecutive rows, every
-// grid-th; a thread's columns are the same for every row.  WREG: its weights
-// stay in registers too.
-template <int V, bool WARP, bool WREG>
+// grid-th; a thread's columns are the same for every row.
+template <int V, bool WARP>
 __global__ void __launch_bounds__(512, 1)
 rmsnorm_bwd_kernel(const NormBwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];         // w, then the rings: stages of dy, x, dres rows
@@ -266,7 +266,7 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     uint4* const wsm = reinterpret_cast<uint4*>(smem);
     uint8_t* const ring = smem + (row_bytes + 127) / 128 * 128 + team * a.stages * 3 * part;
     uint64_t* const bar = bars[team];
-    if (WREG && t < 32) red[0][t] = red[1][t] = 0.0f;        // slots past the last warp stay 0
+    if (!WARP && t < 32) red[0][t] = red[1][t] = 0.0f;       // slots past the last warp stay 0
     if (t == 0) {
         for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
         sm100::fence_barrier_init();
@@ -298,7 +298,8 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
     // KEEP: the row stays in registers between the two passes, so that its
     // stage is refilled between them; rows too long for that are read twice
     constexpr bool KEEP = V <= 2;
-    static_assert(KEEP || !WREG, "the second pass reads the weights from shared memory");
+    // WREG: the weights stay there too (8192 x 7168 80.6 -> 78.2 us)
+    constexpr bool WREG = KEEP && !WARP;
     uint64_t wr[WREG ? V : 1][4];
     if (WREG)
 #pragma unroll
@@ -351,19 +352,16 @@ rmsnorm_bwd_kernel(const NormBwdArgs a) {
                     acc[i][j] = fma2(d[j], mul2(x[k][j], rstd2), acc[i][j]);
                 }
             }
-            float dot;
-            if (WREG) {
+            float dot = warp_sum(lo_of(dot2) + hi_of(dot2));
+            if (!WARP) {
                 // every thread adds the warps' sums itself: one latency, where a
                 // second round of shuffles has five (8192 x 7168: 0.4 us)
-                dot = warp_sum(lo_of(dot2) + hi_of(dot2));
                 if ((t & 31) == 0) red[turn][t >> 5] = dot;
                 __syncthreads();
                 const float4* r = reinterpret_cast<const float4*>(red[turn]);
                 const float4 s0 = r[0], s1 = r[1], s2 = r[2], s3 = r[3];
                 dot = (((s0.x + s0.y) + (s0.z + s0.w)) + ((s1.x + s1.y) + (s1.z + s1.w))) +
                       (((s2.x + s2.y) + (s2.z + s2.w)) + ((s3.x + s3.y) + (s3.z + s3.w)));
-            } else {
-                dot = row_sum<WARP>(lo_of(dot2) + hi_of(dot2), red[turn]);
             }
             if (!WARP && t == 0) {
                 // every thread of the CTA is past its reads of this row (KEEP)
@@ -592,8 +590,8 @@ BwdPlan bwd_plan(int64_t rows, int nvec, int sms) {
     const int warps = (rows + p.batch - 1) / p.batch > 8 * (int64_t)sms ? kBwdMaxWarps : kBwdMaxWarps / 2;
     p.threads = warp ? 32 * warps : ((nvec + p.v - 1) / p.v + 31) / 32 * 32;
     // About 512 threads per SM: with 8192 x 7168 (448 threads) one CTA of four
-    // stages takes 78 us and two of two stages 85 us, with 16384 x 2048 (128
-    // threads) two CTAs 74 us and four 65 us.
+    // stages takes 78 us and two of two stages 85, with 16384 x 2048 (128
+    // threads) four CTAs 46 us, seven of two stages 50.
     p.ctas = warp ? 1 : 512 / p.threads > 4 ? 4 : 512 / p.threads;
     if (nvec > kRingVectors) return p;
     const int row = nvec * 16, stage = 3 * row * p.batch * (warp ? warps : 1), w = (row + 127) / 128 * 128;
@@ -609,9 +607,9 @@ int bwd_grid(int64_t rows, const BwdPlan& p, int nvec, int sms) {
     return (int)min64(tasks, (int64_t)sms * p.ctas);
 }
 
-template <int V, bool WARP, bool WREG = false>
+template <int V, bool WARP>
 cudaError_t launch_bwd(const NormBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t st) {
-    const auto kernel = rmsnorm_bwd_kernel<V, WARP, WREG>;
+    const auto kernel = rmsnorm_bwd_kernel<V, WARP>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3((unsigned)p.threads), p.smem, st, a);
@@ -648,10 +646,6 @@ cudaError_t launch_rmsnorm_backward(const void* dy, const void* x, int64_t ld_x,
         if (nvec <= 32) e = launch_bwd<1, true>(a, p, grid, st);
         else if (nvec <= 64) e = launch_bwd<2, true>(a, p, grid, st);
         else if (nvec <= 128) e = launch_bwd<4, true>(a, p, grid, st);
-        // 8192 x 7168 77.9 us with the weights in registers, 80.6 without; with
-        // several CTAs per SM they cost more than they save (16384 x 2048 66
-        // us with, 47.8 without)
-        else if (nvec <= 1024 && p.ctas == 1) e = launch_bwd<2, false, true>(a, p, grid, st);
         else if (nvec <= 1024) e = launch_bwd<2, false>(a, p, grid, st);
         else if (nvec <= kRingVectors) e = launch_bwd<4, false>(a, p, grid, st);
         else if (nvec <= 2048) e = launch_pdl(rmsnorm_bwd_long_kernel<4>, g, b, 0, st, a);
