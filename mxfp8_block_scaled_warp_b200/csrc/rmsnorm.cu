@@ -582,8 +582,10 @@ BwdPlan bwd_plan(int64_t rows, int nvec, int sms) {
     BwdPlan p{};
     const bool warp = nvec <= 128;
     p.v = warp ? (nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4) : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
-    // short rows are copied several at a time, 2 KB per operand
-    p.batch = warp ? 128 / nvec : 1;
+    // Short rows are copied several at a time, up to 2 KB per operand, unless
+    // that leaves warps without any (505 x 144: 5.9 us with seven rows per
+    // copy).
+    p.batch = warp ? (int)max64(1, min64(128 / nvec, rows / (8 * (int64_t)sms))) : 1;
     // Sixteen warps hide each other's latency where there are rows for them
     // (16384 x 1024 27.6 us, eight warps 30.3); few rows are spread over more
     // CTAs (300 x 1024 5.2 us, sixteen warps 6.0).
