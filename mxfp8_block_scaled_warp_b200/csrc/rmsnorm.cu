@@ -24,10 +24,12 @@
 // into registers 101).
 //
 // Measured at 8192 x 7168: residual, bf16 and MXFP8 out 81 us (6.53 TB/s, the
-// rate of a copy), FP8 without bf16 68 us; backward with dres 77.5 us (6.06
+// rate of a copy), FP8 without bf16 67 us; backward with dres 77.5 us (6.06
 // TB/s), 3 to 4 of them the second kernel's; without dres, a quarter less to
 // move, 74.3: a row's two passes set the pace.  16384 x 1024 backward 26.4 us
 // (5.1 TB/s).  A row of 7168 2.3 us, backward 5.
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -115,8 +117,13 @@ struct NormArgs {
     float* rstd;
 };
 
-template <int FMT, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : V <= 2 ? 1024 : 512)
+// RES: a residual is given.  Without one a thread has half as many bytes on
+// their way, so fewer registers and more CTAs count: 8192 x 7168 to MXFP8 48 us
+// with the residual tested for in the kernel, 43 compiled apart, 40 with room
+// for a third CTA of 512 threads (rows of 1280 to 3584 0 to 6 % slower).  With
+// one, two such CTAs: 8192 x 7168 to FP8 67 us, 74 where the compiler chooses.
+template <int FMT, int V, bool WARP, bool RES>
+__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : V <= 2 ? 1024 : 512, WARP || V != 4 ? 0 : RES ? 2 : 3)
 rmsnorm_quant_kernel(const NormArgs a) {
     __shared__ float red[32];
     pdl_trigger();
@@ -134,14 +141,14 @@ rmsnorm_quant_kernel(const NormArgs a) {
         xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
         if (v < a.nvec) {
             xv[i] = ld_once(xr + v);
-            if (a.res) rv[i] = ld_once(a.res + dense + v);
+            if (RES) rv[i] = ld_once(a.res + dense + v);
         }
     }
     uint64_t s[V][4], sq2 = 0;                              // pairs
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         unpack4(xv[i], s[i]);
-        if (a.res) {
+        if (RES) {
             uint64_t r[4];
             unpack4(rv[i], r);
 #pragma unroll
@@ -209,14 +216,14 @@ rmsnorm_quant_kernel(const NormArgs a) {
     }
 }
 
-template <int FMT>
+template <int FMT, bool RES>
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
     const int nv = a.nvec;
     if (nv <= 128) {
         const dim3 grid((unsigned)((a.rows + kRowWarps - 1) / kRowWarps)), block(32 * kRowWarps);
-        if (nv <= 32) return launch_pdl(rmsnorm_quant_kernel<FMT, 1, true>, grid, block, 0, st, a);
-        if (nv <= 64) return launch_pdl(rmsnorm_quant_kernel<FMT, 2, true>, grid, block, 0, st, a);
-        return launch_pdl(rmsnorm_quant_kernel<FMT, 4, true>, grid, block, 0, st, a);
+        if (nv <= 32) return launch_pdl(rmsnorm_quant_kernel<FMT, 1, true, RES>, grid, block, 0, st, a);
+        if (nv <= 64) return launch_pdl(rmsnorm_quant_kernel<FMT, 2, true, RES>, grid, block, 0, st, a);
+        return launch_pdl(rmsnorm_quant_kernel<FMT, 4, true, RES>, grid, block, 0, st, a);
     }
     // Few rows: latency counts, so a row is spread over as many threads as
     // it has vectors.  Many rows: V = 4 keeps four loads per operand in
@@ -224,10 +231,10 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t st) {
     const dim3 grid((unsigned)a.rows);
     const auto threads = [&](int v) { return dim3((unsigned)(((nv + v - 1) / v + 31) / 32 * 32)); };
     const bool few = a.rows < 2 * sms;
-    if (few && nv <= 1024) return launch_pdl(rmsnorm_quant_kernel<FMT, 1, false>, grid, threads(1), 0, st, a);
-    if (few && nv <= 2048) return launch_pdl(rmsnorm_quant_kernel<FMT, 2, false>, grid, threads(2), 0, st, a);
-    if (nv <= 2048) return launch_pdl(rmsnorm_quant_kernel<FMT, 4, false>, grid, threads(4), 0, st, a);
-    return launch_pdl(rmsnorm_quant_kernel<FMT, 8, false>, grid, threads(8), 0, st, a);
+    if (few && nv <= 1024) return launch_pdl(rmsnorm_quant_kernel<FMT, 1, false, RES>, grid, threads(1), 0, st, a);
+    if (few && nv <= 2048) return launch_pdl(rmsnorm_quant_kernel<FMT, 2, false, RES>, grid, threads(2), 0, st, a);
+    if (nv <= 2048) return launch_pdl(rmsnorm_quant_kernel<FMT, 4, false, RES>, grid, threads(4), 0, st, a);
+    return launch_pdl(rmsnorm_quant_kernel<FMT, 8, false, RES>, grid, threads(8), 0, st, a);
 }
 
 // ------------------------------------------------------------------ backward
@@ -624,8 +631,12 @@ cudaError_t launch_rmsnorm_quantize(int fmt, const void* x, int64_t ld_x, const 
                                     float* rstd, int sms, cudaStream_t st) {
     const NormArgs a{(const uint4*)x, ld_x / 8, (const uint4*)residual, (const uint4*)weight, rows, (int)(cols / 8),
                      (float)cols, eps, (uint4*)h, (uint4*)y, (uint2*)q, scales, rstd};
-    if (!q) return launch_norm<kNormNone>(a, sms, st);
-    return fmt == FPQ_FP8_1x128 ? launch_norm<kNormFp8>(a, sms, st) : launch_norm<kNormMx>(a, sms, st);
+    const auto launch = [&](auto res) {
+        constexpr bool RES = decltype(res)::value;
+        if (!q) return launch_norm<kNormNone, RES>(a, sms, st);
+        return fmt == FPQ_FP8_1x128 ? launch_norm<kNormFp8, RES>(a, sms, st) : launch_norm<kNormMx, RES>(a, sms, st);
+    };
+    return residual ? launch(std::true_type()) : launch(std::false_type());
 }
 
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, int sms) {
