@@ -35,7 +35,7 @@
 // than 32 such keys, which take equal logits, and for groups too near to
 // tell; throughout it took 51 us for 16384 tokens.  Measured for eight of 256,
 // 16384 tokens, fp32: 13.0 us without a bias (1.4 TB/s), sigmoid with one
-// 18.4, in eight groups 27.4 (at 70% of the issue slots), softmax with a bias
+// 18.4, in eight groups 27.4 (at 78% of the issue slots), softmax with a bias
 // 26.4.
 #include <type_traits>
 
