@@ -517,8 +517,9 @@ FPQ_API fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const
  *   rstd       fp32 [rows] (optional output, kept for the backward pass)
  *
  * At least one of y and q.  The codes are those of y before its rounding to
- * bf16 (FP8_1x128: of y times the scale's fp32 reciprocal, within 2^-23 of the
- * quotient).  Other overlaps between inputs and outputs are not allowed.
+ * bf16, by the rule of fpq_quantize_block (FP8_1x128: the rounding of the
+ * correctly rounded fp32 quotient of y and the scale).  Other overlaps between
+ * inputs and outputs are not allowed.
  *
  * Requires 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768] (of 128 with
  * FPQ_FP8_1x128 codes, of 32 with FPQ_MXFP8), ld_x >= cols a multiple of 8,

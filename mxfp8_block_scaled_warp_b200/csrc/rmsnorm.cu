@@ -24,7 +24,7 @@
 // into registers 101).
 //
 // Measured at 8192 x 7168: residual, bf16 and MXFP8 out 81 us (6.53 TB/s, the
-// rate of a copy), FP8 without bf16 67 us; backward with dres 77.5 us (6.06
+// rate of a copy), FP8 without bf16 68.5 us; backward with dres 77.5 us (6.06
 // TB/s), 3 to 4 of them the second kernel's; without dres, a quarter less to
 // move, 74.3: a row's two passes set the pace.  16384 x 1024 backward 26.4 us
 // (5.1 TB/s).  A row of 7168 2.3 us, backward 5.
@@ -102,6 +102,22 @@ __device__ __forceinline__ int mx_exponent_f32(uint32_t a) {
     return max(-127, min(127, E - 127 - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
 }
 
+// -fp32(y / s) of a pair, for the codes, from n = fp32(-1 / s): the product
+// y n and one correction by its remainder, which the fused multiply-add
+// leaves exact (Markstein's division).  Its E4M3 code is the negated code of
+// the correctly rounded quotient: for every mantissa of s and the nine values
+// of y around each midpoint of codes, 1.2e9 cases, the quotients were compared
+// and are equal; away from midpoints the last place decides nothing.  Negated,
+// so that a zero keeps its sign.  For 2^-92 <= s < infinity: the remainder is
+// exact for |y| >= 2^-103, and a smaller y is below half the smallest code.
+// Two more paired instructions per pair than the product alone (8192 x 7168
+// with a residual 68.5 us instead of 67.2, without one 47.8 instead of 44.8).
+__device__ __forceinline__ bool corrected_quotients_ok(float s) { return s >= 0x1p-92f && s < INFINITY; }
+__device__ __forceinline__ uint64_t negated_quotients(uint64_t y, uint64_t s, uint64_t n) {
+    const uint64_t q = mul2(y, n);
+    return fma2(fma2(q, s, y), n, q);
+}
+
 struct NormArgs {
     const uint4* x;        // row r at x + r ld
     int64_t ld;            // in vectors of 8 elements
@@ -121,7 +137,8 @@ struct NormArgs {
 // their way, so fewer registers and more CTAs count: 8192 x 7168 to MXFP8 48 us
 // with the residual tested for in the kernel, 43 compiled apart, 40 with room
 // for a third CTA of 512 threads (rows of 1280 to 3584 0 to 6 % slower).  With
-// one, two such CTAs: 8192 x 7168 to FP8 67 us, 74 where the compiler chooses.
+// one, two such CTAs: 8192 x 7168 to FP8 67 us, 74 where the compiler chooses
+// (before the codes took the correction of negated_quotients).
 template <int FMT, int V, bool WARP, bool RES>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : V <= 2 ? 1024 : 512, WARP || V != 4 ? 0 : RES ? 2 : 3)
 rmsnorm_quant_kernel(const NormArgs a) {
@@ -181,21 +198,19 @@ rmsnorm_quant_kernel(const NormArgs a) {
         if (FMT == kNormFp8) {
             top = group_max<16>(in ? top : 0u);             // the 16 lanes of a 128-element tile, in or out together
             const float sc = top ? __fdiv_rn(__uint_as_float(top), 448.0f) : 1.0f;
-            uint32_t c[2];
-            if (reciprocal_ok(sc)) {
-                // a quotient by the scale as a product with its reciprocal: 2^-23
-                // off at most, less than y itself
-                const float r = __frcp_rn(sc);
-                const uint64_t r2 = pack2(r, r);
-                c[0] = e4m3x4_of_pairs(mul2(s[i][0], r2), mul2(s[i][1], r2));
-                c[1] = e4m3x4_of_pairs(mul2(s[i][2], r2), mul2(s[i][3], r2));
+            uint64_t d[4];
+            uint32_t flip = 0;
+            if (corrected_quotients_ok(sc)) {
+                const float n = -__frcp_rn(sc);
+                const uint64_t n2 = pack2(n, n), sc2 = pack2(sc, sc);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = negated_quotients(s[i][j], sc2, n2);
+                flip = 0x80808080u;
             } else {
-                uint64_t d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = pack2(__fdiv_rn(lo_of(s[i][j]), sc), __fdiv_rn(hi_of(s[i][j]), sc));
-                c[0] = e4m3x4_of_pairs(d[0], d[1]);
-                c[1] = e4m3x4_of_pairs(d[2], d[3]);
             }
+            const uint32_t c[2] = {e4m3x4_of_pairs(d[0], d[1]) ^ flip, e4m3x4_of_pairs(d[2], d[3]) ^ flip};
             if (in) {
                 st_v2(a.q + dense + v, make_uint2(c[0], c[1]));
                 if ((v & 15) == 0) static_cast<float*>(a.scales)[(dense + v) >> 4] = sc;

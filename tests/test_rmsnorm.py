@@ -271,3 +271,26 @@ def test_far_rows(fpq):
     # each within 64 steps of 2^-24 of the magnitudes' sum
     size = (dy.double() * part.double() * rstd.double()[:, None]).abs().sum(0)
     assert torch.all((dw.double() - dw_near.double()).abs() <= 2.0 ** -17 * size)
+
+
+@pytest.mark.parametrize("rows,cols,residual", [(4099, 512, False), (700, 1024, True), (3, 7168, False), (700, 7168, True),
+                                                (310, 16384, False), (310, 32768, True)])
+def test_fp8_codes_are_those_of_the_fp32_quotient(fpq, rows, cols, residual):
+    """Bit for bit the rule of quantize(): scale = fp32(amax / 448), code = the
+    rounding of fp32(y / scale), for the fp32 y that the kernel forms.  bf16
+    products meet the midpoints between codes often, so the quotient's last
+    place counts."""
+    x, w, r = _data(rows, cols, 61, residual=residual)
+    x[0, :256] = -0.0                                                # zeros of both signs
+    w[5], w[6] = 0.0, -0.0
+    if residual:
+        r[0, :256] = -0.0
+    out = fpq.rmsnorm_quantize(x, w, fpq.FP8_1x128, residual=r, want_rstd=True)
+    s = x.float() + r.float() if residual else x.float()
+    t = (s * out.rstd[:, None] * w.float()).view(rows, cols // 128, 128)
+    top = t.abs().amax(-1)
+    # a tensor of divisors: by a Python number torch multiplies with its reciprocal
+    scale = torch.where(top == 0, torch.ones_like(top), top / torch.full_like(top, 448.0))
+    assert torch.equal(out.scales, scale)
+    want = (t / scale[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).view(rows, cols)
+    assert torch.equal(out.q, want), f"{(out.q != want).sum().item()} codes of {want.numel()}"
