@@ -166,13 +166,13 @@ moe_gate_kernel(const GateArgs a) {
         if (mx == -INFINITY) return x == x ? 0.0f : x;
         return __fdividef(__expf(x - mx), sum);
     };
-    // At least twice the error of a sum of n fp32 keys near `key`: a sigmoid is
-    // within 2^-20; a softmax within 2^-18 of the row's largest (1 / sum), as
-    // its sum of up to 1024 terms goes through at most 37 additions in a row;
-    // adding the bias costs half a step.
+    // At least twice the error of an fp32 key: a sigmoid is within 2^-20; a
+    // softmax within 2^-18 of the row's largest (1 / sum), as its sum of up to
+    // 1024 terms goes through at most 37 additions in a row; adding the bias
+    // costs half a step.
     const float error = SIGMOID ? 0x1p-20f : sum > 0.0f ? __fdividef(0x1p-18f, sum) : 0.0f;
-    const auto slack = [&](float key, int n) {
-        return fabsf(key) < INFINITY ? 2.0f * (float)n * (error + 0x1p-23f * fabsf(key)) : 0.0f;
+    const auto slack = [&](float key) {
+        return fabsf(key) < INFINITY ? 2.0f * (error + 0x1p-23f * fabsf(key)) : 0.0f;
     };
     double sum64 = 0.0;
     const auto need64 = [&]() {                             // warp-uniform
@@ -225,7 +225,10 @@ moe_gate_kernel(const GateArgs a) {
         uint32_t gkey = holds ? pattern(rank) : kTaken;
         // each group counts the ranks above its own; only where two are too
         // near to tell are the best taken one after the other
-        const float own = value(gkey), reach = slack(own, a.group_top);
+        // twice the rank's error: each key has its own, by its own magnitude,
+        // which the sum may fall far below; the addition's step is within them
+        const float own = value(gkey);
+        const float reach = fabsf(own) < INFINITY ? slack(first) + (a.group_top == 2 ? slack(second) : 0.0f) : 0.0f;
         int above = 0;
         bool close = false;
 #pragma unroll 4
@@ -240,8 +243,8 @@ moe_gate_kernel(const GateArgs a) {
         if (!apart) open = 0;
         for (int c = apart ? a.topk_group : 0; c < a.topk_group; ++c) {
             const uint32_t m = __reduce_max_sync(kFull, gkey);
-            const float least = value(m) - slack(value(m), a.group_top);
-            const bool near = gkey != kTaken && (gkey == m || (gkey > kNaN && value(gkey) >= least));
+            const float most_reach = __uint_as_float(__reduce_max_sync(kFull, gkey == m ? __float_as_uint(reach) : 0u));
+            const bool near = gkey != kTaken && (gkey == m || (gkey > kNaN && value(m) - own <= fmaxf(reach, most_reach)));
             const uint32_t cand = __ballot_sync(kFull, near);
             int best = __ffs(cand) - 1;
             if (cand & (cand - 1)) {
@@ -294,7 +297,7 @@ moe_gate_kernel(const GateArgs a) {
         from += (u.x >= top) + (u.y >= top) + (u.z >= top) + (u.w >= top);
     }
     uint32_t bound = __reduce_max_sync(kFull, from >= a.topk ? top : 0u);
-    if (a.bias && bound > kNaN) bound = pattern(value(bound) - slack(value(bound), 1));
+    if (a.bias && bound > kNaN) bound = pattern(value(bound) - slack(value(bound)));
     bound = max(bound, kNaN);                                // there are topk experts inside the chosen groups
     int count = 0;
 #pragma unroll
@@ -315,7 +318,7 @@ moe_gate_kernel(const GateArgs a) {
         place = lane < count ? 0 : 32;
         bool near = false;
         if (a.bias) {
-            const float v = value(c.x), reach = slack(v, 1);
+            const float v = value(c.x), reach = slack(v);
 #pragma unroll 4
             for (int j = 0; j < count; ++j) {
                 const uint32_t k = __shfl_sync(kFull, c.x, j);
@@ -350,7 +353,7 @@ moe_gate_kernel(const GateArgs a) {
             for (int i = 1; i < VPT; ++i) t = max(t, key[i]);
             const uint32_t m = __reduce_max_sync(kFull, t);
             uint32_t least = m;
-            if (a.bias && m > kNaN) least = pattern(value(m) - slack(value(m), 1));
+            if (a.bias && m > kNaN) least = pattern(value(m) - slack(value(m)));
             int n = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) n += key[i] >= least;

@@ -303,3 +303,35 @@ def test_backward_of_the_full_softmax_with_an_id_named_twice(fpq, experts, dtype
     size = p * (v.abs().sum(1, keepdim=True))
     rel = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
     assert torch.all((d.double() - want).abs() <= rel * want.abs() + 2.0 ** -15 * size + 1e-37)
+
+
+@pytest.mark.parametrize("score", [moe.SOFTMAX, moe.SIGMOID])
+@pytest.mark.parametrize("size", [10.0, 100.0, 1000.0])
+@pytest.mark.parametrize("n_group,topk_group,topk", [(8, 4, 8), (32, 8, 8)])
+def test_groups_whose_best_keys_cancel(fpq, score, size, n_group, topk_group, topk):
+    """One expert of a group with a large bias and the others with the
+    opposite one: the keys' fp32 steps are those of the bias, their sum is of
+    the order of a score."""
+    bias = torch.full((256,), -size, device="cuda")
+    bias[torch.arange(n_group, device="cuda") * (256 // n_group) + 3] = size
+    _check(_logits(16384, 256, 41), topk, bias, score, n_group, topk_group, 2)
+    # of one group only: the others' ranks are compared with it and with each other
+    one = torch.zeros((256,), device="cuda")
+    one[:256 // n_group] = -size
+    one[3] = size
+    _check(_logits(4096, 256, 42), topk, one, score, n_group, topk_group, 2)
+
+
+def test_a_group_ahead_by_less_than_its_keys_steps(fpq):
+    """Two groups whose fp32 ranks are in the wrong order by a step of the
+    best key (2^-13 at 1024), while the exact ranks are 2^-20 apart."""
+    t = 2.0 ** -20
+    p = torch.full((3, 8), 0.25, dtype=torch.float64)
+    p[:, 0], p[:, 1] = 0.5 + 2.0 ** -14 + t, 0.5                    # 1 + 2^-14 + t; in fp32 1 + 2^-13
+    p[:, 4], p[:, 5] = 0.5 + 2.0 ** -14 - t, 0.5 + 3 * t            # 1 + 2^-14 + 2 t; in fp32 1
+    p[1, 5] = 0.5                                                    # behind the first
+    p[2] = p[2].roll(4)
+    lg = torch.log(p / (1 - p)).float().cuda()
+    bias = torch.tensor([1024.0, -1024, -1024, -1024] * 2, device="cuda")
+    ids, _ = _check(lg, 2, bias, moe.SIGMOID, 2, 1, 2)
+    assert torch.equal((ids[:, 0] // 4).cpu(), torch.tensor([1, 0, 0], dtype=torch.int32))
