@@ -349,11 +349,13 @@ cudaError_t gemv(GemvArgs a, cudaStream_t st) {
     a.chunk = fit < groups ? fit : groups;
     const int blocks = a.chunk * kGroup;
     const int smem = a.cols * (blocks * 256 + 64) + blocks * 8 * TILES * (int)sizeof(float);
-    const auto kernel = gemv_nvfp4_kernel<TILES, CTAS, EXPERTS>;
-    if (smem > 32 * 1024) {                                  // with the static arrays, past what needs no opt-in
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    // x and the columns' padding, and a factor per block and column of a tile:
+    // the most blocks are those of a single column
+    constexpr int most = kXBytes / CTAS + 64 * 8 * TILES + kXBytes / CTAS / 256 * 8 * TILES * (int)sizeof(float);
+    static_assert(CTAS * (most + 20 * 1024) <= 227 * 1024, "with the static arrays, an SM's shared memory");
+    constexpr auto kernel = gemv_nvfp4_kernel<TILES, CTAS, EXPERTS>;
+    const cudaError_t e = allow_shared_memory<kernel, most>();
+    if (e != cudaSuccess) return e;
     const int64_t tiles = (a.n + 15) / 16;
     return launch_pdl(kernel, dim3((unsigned)((tiles + a.wr - 1) / a.wr), (unsigned)(EXPERTS ? a.m : 1)),
                       dim3(32u * a.wk * a.wr), smem, st, a);

@@ -5,6 +5,8 @@
 // headers that those include.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -46,6 +48,23 @@ cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const vo
 cudaError_t launch_gemv_nvfp4(const void* x, int64_t m, int x_div, int tokens, const int32_t* ids, int experts,
                               const void* wq, const void* ws, const float* wg, int64_t n, int64_t k, void* y,
                               int y_f32, uint32_t* err, int sms, cudaStream_t st);
+
+// Lets the kernel take up to `Bytes` of dynamic shared memory on the current
+// device, once.  The attribute is the function's, not the launch's: it is a
+// constant, so that host threads with calls of different sizes cannot take
+// from each other what they need.
+template <auto Kernel, int Bytes>
+cudaError_t allow_shared_memory() {
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // two E4M3 codes (bits 0..15) -> packed f16x2, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c2) {

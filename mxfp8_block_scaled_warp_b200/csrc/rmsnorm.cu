@@ -633,8 +633,8 @@ int bwd_grid(int64_t rows, const BwdPlan& p, int nvec, int sms) {
 
 template <int V, bool WARP>
 cudaError_t launch_bwd(const NormBwdArgs& a, const BwdPlan& p, int grid, cudaStream_t st) {
-    const auto kernel = rmsnorm_bwd_kernel<V, WARP>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    constexpr auto kernel = rmsnorm_bwd_kernel<V, WARP>;
+    const cudaError_t e = allow_shared_memory<kernel, kBwdSmem>();
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3((unsigned)p.threads), p.smem, st, a);
 }

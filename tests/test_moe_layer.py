@@ -2,6 +2,8 @@
 norm -> gate -> dispatch -> grouped product -> combination and back, and the
 decoding form with NVFP4 weights; on a side stream, on two streams at once
 and captured into graphs."""
+import threading
+
 import pytest
 import torch
 
@@ -185,3 +187,76 @@ def test_side_stream_and_two_at_once(fpq):
         for u, v in zip(one, want):
             assert torch.equal(u, v)
     assert fpq.fpq_get_device_error() == 0
+
+
+def test_two_host_threads(fpq):
+    """The C entry points from two threads, with shapes of one kernel that need
+    different amounts of shared memory: every call is accepted and right."""
+    w = fpq.quantize(_normal((2048, 7168), 0.02, 100), fpq.NVFP4)
+    x = _normal((16, 7168), 1, 101)
+    lib = fpq.load()                                 # the library's functions themselves: the calls overlap often
+
+    def product(m):
+        y = torch.empty((m, 2048), dtype=BF16, device="cuda")
+        args = [x.data_ptr(), m, *(p.data_ptr() for p in w), 2048, 7168, y.data_ptr(), fpq.OUT_BF16, None]
+        return lambda: lib.fpq_gemv_nvfp4(*args), y
+
+    def norm(rows, cols):
+        a, wt, dy = _normal((rows, cols), 1, 102), _normal((cols,), 0.1, 103) + 1, _normal((rows, cols), 1, 104)
+        rstd = torch.ones((rows,), device="cuda")
+        dx, dw = torch.empty_like(a), torch.empty((cols,), device="cuda")
+        ws = torch.empty((fpq.fpq_rmsnorm_backward_workspace_bytes(rows, cols),), dtype=torch.uint8, device="cuda")
+        keep = (dy, a, wt, rstd, dx, dw, ws)
+        args = [dy.data_ptr(), a.data_ptr(), cols, wt.data_ptr(), rstd.data_ptr(), None, rows, cols, dx.data_ptr(),
+                dw.data_ptr(), ws.data_ptr(), ws.numel(), None]
+        return lambda: (lib.fpq_rmsnorm_backward(*args), keep)[0], dx
+
+    for pair in ((product(8), product(3)), (product(16), product(9)), (norm(20, 1024), norm(20, 528)),
+                 (norm(20, 7168), norm(20, 1040))):
+        want = []
+        for call, out in pair:
+            assert call() == 0
+            want.append(out.clone())
+            out.zero_()
+        torch.cuda.synchronize()
+        refused, start = [0, 0], threading.Barrier(2)
+
+        def many(i):
+            start.wait()
+            for _ in range(10000):
+                if pair[i][0]() != 0:
+                    refused[i] += 1
+
+        threads = [threading.Thread(target=many, args=(i,)) for i in range(2)]
+        for th in threads:
+            th.start()
+        for th in threads:
+            th.join()
+        torch.cuda.synchronize()
+        assert refused == [0, 0]
+        for (_, out), u in zip(pair, want):
+            assert torch.equal(out, u)
+
+
+def test_large_and_small_shapes_in_one_graph(fpq):
+    """A call that needs much shared memory captured before one of the same
+    kernel that needs little."""
+    w = fpq.quantize(_normal((2048, 7168), 0.02, 110), fpq.NVFP4)
+    x, wn = _normal((20, 7168), 1, 111), _normal((7168,), 0.1, 112) + 1
+    rstd = torch.ones((20,), device="cuda")
+
+    def step():
+        big = fpq.gemv_nvfp4(x[:8], *w), fpq.rmsnorm_backward(x, x, wn, rstd)[0]
+        narrow, wn2 = x[:, :1040].contiguous(), wn[:1040].contiguous()
+        return (*big, fpq.gemv_nvfp4(x[:3], *w), fpq.rmsnorm_backward(narrow, narrow, wn2, rstd)[0])
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for t in out:
+        t.zero_()
+    g.replay()
+    for u, v in zip(out, want):
+        assert torch.equal(u, v)
