@@ -518,8 +518,8 @@ FPQ_API fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const
  *
  * At least one of y and q.  The codes are those of y before its rounding to
  * bf16, by the rule of fpq_quantize_block (FP8_1x128: the rounding of the
- * correctly rounded fp32 quotient of y and the scale).  Other overlaps between
- * inputs and outputs are not allowed.
+ * correctly rounded fp32 quotient of y and the scale, which is 1 where amax /
+ * 448 rounds to 0).  Other overlaps between inputs and outputs are not allowed.
  *
  * Requires 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768] (of 128 with
  * FPQ_FP8_1x128 codes, of 32 with FPQ_MXFP8), ld_x >= cols a multiple of 8,

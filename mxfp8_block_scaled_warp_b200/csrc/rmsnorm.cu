@@ -197,7 +197,8 @@ rmsnorm_quant_kernel(const NormArgs a) {
         if (a.y && in) st_v4(a.y + dense + v, pack4(s[i]));
         if (FMT == kNormFp8) {
             top = group_max<16>(in ? top : 0u);             // the 16 lanes of a 128-element tile, in or out together
-            const float sc = top ? __fdiv_rn(__uint_as_float(top), 448.0f) : 1.0f;
+            // up to 224 steps of the smallest number the quotient rounds to 0
+            const float sc = top > 224u ? __fdiv_rn(__uint_as_float(top), 448.0f) : 1.0f;
             uint64_t d[4];
             uint32_t flip = 0;
             if (corrected_quotients_ok(sc)) {

@@ -294,3 +294,25 @@ def test_fp8_codes_are_those_of_the_fp32_quotient(fpq, rows, cols, residual):
     assert torch.equal(out.scales, scale)
     want = (t / scale[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).view(rows, cols)
     assert torch.equal(out.q, want), f"{(out.q != want).sum().item()} codes of {want.numel()}"
+
+
+def test_fp8_tile_whose_scale_rounds_to_zero(fpq):
+    """amax / 448 of a magnitude below 224 steps of fp32 rounds to 0: the
+    tile's scale is 1 then and its codes 0, as for a tile of zeros."""
+    x = torch.zeros((2, 384), dtype=BF16, device="cuda")
+    x[0, 130], x[0, 131], x[0, 300] = 2.0 ** -60, -2.0 ** -60, 1.0
+    x[1, 0], x[1, 200] = 2.0 ** -60, float("nan")
+    w = torch.ones((384,), dtype=BF16, device="cuda")
+    for residual in (None, torch.zeros_like(x)):
+        # sum of squares 1: rstd is about 19.6, y 627 steps of 2^-149, its scale one step
+        w[128:256] = 2.0 ** -84
+        out = fpq.rmsnorm_quantize(x, w, fpq.FP8_1x128, residual=residual)
+        q, s = out.q.cpu(), out.scales.cpu()
+        assert s[0].tolist()[:2] == [1.0, 2.0 ** -149] and q[0, 130:132].tolist() == [0x7E, 0xFE]
+        q[0, 130:132] = 0
+        assert torch.all(q[0, :256] == 0) and q[0, 300] == 0x7E
+        w[128:256] = 2.0 ** -89                                      # y 20 steps
+        out = fpq.rmsnorm_quantize(x, w, fpq.FP8_1x128, residual=residual)
+        q, s = out.q.cpu(), out.scales.cpu()
+        assert s[0].tolist()[:2] == [1.0, 1.0] and torch.all(q[0, :256] & 0x7F == 0) and q[0, 300] == 0x7E
+        assert torch.all(torch.isnan(s[1])) and torch.all(q[1] & 0x7F == 0x7F)
