@@ -664,8 +664,8 @@ FPQ_API fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype
  * weights, the form that decoding takes (the activations stay bf16):
  *   y[m, n] = g sum_k x[m, k] e2m1(W[n, k]) e4m3(S[n, k/16])
  * Weights are decoded exactly, sums are fp32, g multiplies the sum.  Elements
- * of x are exact down to 2^-32 of the largest magnitude of their 128 (columns
- * 128 i to 128 i + 127); smaller ones are rounded by at most 2^-40 of it.
+ * of x are exact down to 2^-31 of the largest magnitude of their 128 (columns
+ * 128 i to 128 i + 127); smaller ones are rounded by at most 2^-39 of it.
  *
  * Dense form:
  *   x            bf16 [m, k], 0 <= m <= 16

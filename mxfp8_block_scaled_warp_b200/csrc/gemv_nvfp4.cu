@@ -16,8 +16,9 @@
 // have one type, so x becomes f16 too: per row and block of 128 it is
 // multiplied by the power of two that takes the block's largest magnitude to
 // [2^14, 2^15), and the block's fp32 sum is multiplied back.  That is exact
-// for every element within 2^-32 of the block's largest; a smaller one is
-// rounded by at most 2^-40 of the largest, far below what the fp32 sum keeps
+// for every element within 2^-31 of the block's largest (eight bits above
+// f16's smallest step, 2^-24); a smaller one is rounded by at most half a
+// step, 2^-39 of the largest, far below what the fp32 sum keeps
 // of it.  (With bf16 as the common type nothing of x is rounded, but a pair
 // of codes takes four instructions instead of two: 60 us against 37 for one
 // row, 32768 x 7168, at that step.)

@@ -200,3 +200,27 @@ def test_experts_named_several_times(fpq, tokens, topk, experts):
         ids = ids.int().cuda()
         y = fpq.gemv_nvfp4(x, wq, ws, wg, ids=ids, out_dtype=torch.float32)
         _inside(y, x.double(), w[ids.long()], torch.float32)
+
+
+@pytest.mark.parametrize("m", [1, 9])
+def test_small_elements_beside_a_large_one(fpq, m):
+    """x is exact down to 2^-31 of the largest of its 128 columns, and within
+    2^-39 of that below: a 1 under zero weights, and small elements with all
+    their eight bits under the others."""
+    n, k = 32, 256
+    wq = torch.full((n, k // 2), 0x22, dtype=torch.uint8, device="cuda")               # ones
+    wq[:, 0] = 0x20                                                                    # 0 at column 0
+    ws = torch.full((n, k // 16), 0x38, dtype=torch.uint8, device="cuda")              # 1
+    wg = torch.ones((1,), device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(m)
+    for top in (1.0, 1.9921875):
+        for power in range(24, 48):
+            x = torch.zeros((m, k), device="cuda")
+            x[:, 0] = top
+            at = 1 + torch.randint(0, 127, (m,), generator=g, device="cuda")
+            small = (1 + torch.randint(0, 128, (m,), generator=g, device="cuda") / 128) * 2.0 ** -power
+            x[torch.arange(m, device="cuda"), at] = small
+            x = x.to(torch.bfloat16)
+            y = fpq.gemv_nvfp4(x, wq, ws, wg, out_dtype=torch.float32)
+            err = (y.double() - small.double()[:, None]).abs()
+            assert torch.all(err <= (2.0 ** -39 * top if power > 31 else 0)), (top, power, err.max().item())
