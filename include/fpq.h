@@ -603,8 +603,9 @@ FPQ_API fpq_status fpq_moe_gate(const void* logits, int32_t logits_dtype, const 
  * fpq_moe_gate_backward -- gradient of the logits for the gradient dweights
  * fp32 [tokens, topk] of the weights (the choice and the bias carry none).
  * dlogits has the logits' type and shape; every element is written.  An id
- * out of [0, E) raises FPQ_ERR_DEVICE_BAD_INPUT and is dropped.  The other
- * arguments as in the forward call, whose ids these are.
+ * out of [0, E) raises FPQ_ERR_DEVICE_BAD_INPUT and is dropped.  dlogits must
+ * not overlap logits (FPQ_ERR_INVALID_ARG).  The other arguments as in the
+ * forward call, whose ids these are.
  */
 FPQ_API fpq_status fpq_moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* ids,
                                          const float* dweights, int64_t tokens, int32_t num_experts, int32_t score,

@@ -76,6 +76,11 @@ const DeviceState* device_state(fpq_status* st) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return p < q + (uint64_t)b_bytes && q < p + (uint64_t)a_bytes;
+}
+
 fpq_status check_ptrs(std::initializer_list<const void*> ps) {
     for (const void* p : ps) {
         if (!p) { set_detail("null pointer argument"); return FPQ_ERR_INVALID_ARG; }
@@ -660,6 +665,12 @@ fpq_status fpq_moe_gate_backward(const void* logits, int32_t logits_dtype, const
     }
     if (tokens == 0) return FPQ_OK;
     if ((st = check_ptrs({logits, ids, dweights, dlogits})) != FPQ_OK) return st;
+    // a lane zeroes a row while others may still read its chosen logits
+    const int64_t bytes = tokens * num_experts * (logits_dtype == FPQ_OUT_F32 ? 4 : 2);
+    if (overlap(logits, bytes, dlogits, bytes)) {
+        set_detail("dlogits must not overlap logits");
+        return FPQ_ERR_INVALID_ARG;
+    }
     const DeviceState* d = device_state(&st);
     if (!d) return st;
     return from_cuda(fpq::launch_moe_gate_backward(logits, logits_dtype == FPQ_OUT_F32, ids, dweights, tokens,

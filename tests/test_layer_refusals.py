@@ -180,3 +180,16 @@ def test_counts_whose_product_passes_64_bits(lib):
     assert lib.fpq_moe_combine(P, 0, 128, P, P, far, 8, 64, P, P, 0, None) == INVALID
     assert lib.fpq_moe_combine_backward(P, 1, P, 0, 128, P, P, far, 8, 64, P, P, None) == INVALID
     assert lib.fpq_moe_pair_rows(P, far, 8, 64, P, 1 << 30, P, P, None) == INVALID
+
+
+def test_gate_backward_refuses_a_gradient_over_its_logits(lib):
+    def call(logits, dlogits, dtype=0):
+        return lib.fpq_moe_gate_backward(logits, dtype, P, P, 16, 64, 0, 8, 1, 1.0, dlogits, None)
+
+    size = 16 * 64 * 2
+    for dtype, n in ((0, size), (1, 2 * size)):
+        for shift in (0, 16, n - 16):
+            assert call(P, P + shift, dtype) == INVALID and b"overlap" in lib.fpq_last_error_detail()
+            assert call(P + shift, P, dtype) == INVALID and b"overlap" in lib.fpq_last_error_detail()
+    if not torch.cuda.is_available():                        # beside each other: as far as the device
+        assert call(P, P + size) == UNSUPPORTED and call(P + size, P) == UNSUPPORTED
