@@ -647,10 +647,15 @@ FPQ_API fpq_status fpq_moe_pair_rows(const int32_t* topk_ids, int64_t tokens, in
  * as they were.  A row may be named by one pair only.  dy must not overlap y
  * or dout.
  *
+ * fpq_moe_combine_backward_full -- the same, and zeros in the rows that no
+ * pair names: every row of dy is written.
+ *   workspace  4 y_rows bytes, caller-owned, whatever they hold; not needed
+ *              without rows
+ *
  * Requires tokens >= 0, 1 <= topk <= 32, tokens * topk < 2^31, hidden a
  * positive multiple of 8 up to 2^24, 0 <= y_rows < 2^31 (>= tokens * topk without rows),
  * every pointer 16-byte aligned.  Errors: FPQ_ERR_INVALID_ARG,
- * FPQ_ERR_ALIGNMENT, FPQ_ERR_CUDA.
+ * FPQ_ERR_ALIGNMENT, FPQ_ERR_WORKSPACE, FPQ_ERR_CUDA.
  */
 FPQ_API fpq_status fpq_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, const int32_t* rows,
                                    const float* weights, int64_t tokens, int32_t topk, int64_t hidden,
@@ -659,6 +664,11 @@ FPQ_API fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype
                                             int64_t y_rows, const int32_t* rows, const float* weights,
                                             int64_t tokens, int32_t topk, int64_t hidden, void* dy, float* dweights,
                                             void* stream);
+FPQ_API fpq_status fpq_moe_combine_backward_full(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype,
+                                                 int64_t y_rows, const int32_t* rows, const float* weights,
+                                                 int64_t tokens, int32_t topk, int64_t hidden, void* dy,
+                                                 float* dweights, void* workspace, size_t workspace_bytes,
+                                                 void* stream);
 
 /*
  * fpq_gemv_nvfp4, fpq_moe_gemv_nvfp4 -- products of a few bf16 rows with NVFP4

@@ -44,6 +44,7 @@ __all__ = [
     "scale_shape", "code_shape", "gemm_bf16", "qat_backward",
     "fpq_rmsnorm_quantize", "fpq_rmsnorm_backward_workspace_bytes", "fpq_rmsnorm_backward",
     "fpq_moe_gate", "fpq_moe_gate_backward", "fpq_moe_pair_rows", "fpq_moe_combine", "fpq_moe_combine_backward",
+    "fpq_moe_combine_backward_full",
     "fpq_gemv_nvfp4", "fpq_moe_gemv_nvfp4", "MOE_SOFTMAX", "MOE_SIGMOID",
     "RmsNorm", "rmsnorm_quantize", "rmsnorm_backward", "gemv_nvfp4",
 ]
@@ -118,6 +119,7 @@ def _load() -> ctypes.CDLL:
         "fpq_moe_pair_rows": (I32, [P, I64, I32, I32, P, SZ, P, P, P]),
         "fpq_moe_combine": (I32, [P, I32, I64, P, P, I64, I32, I64, P, P, I32, P]),
         "fpq_moe_combine_backward": (I32, [P, I32, P, I32, I64, P, P, I64, I32, I64, P, P, P]),
+        "fpq_moe_combine_backward_full": (I32, [P, I32, P, I32, I64, P, P, I64, I32, I64, P, P, P, SZ, P]),
         "fpq_gemv_nvfp4": (I32, [P, I64, P, P, P, I64, I64, P, I32, P]),
         "fpq_moe_gemv_nvfp4": (I32, [P, I32, P, I64, I32, I32, P, P, P, I64, I64, P, I32, P]),
     }
@@ -370,6 +372,15 @@ def fpq_moe_combine_backward(dout, dout_dtype, y, y_dtype, y_rows, rows, weights
     _check(load().fpq_moe_combine_backward(_ptr(dout), dout_dtype, _ptr(y), y_dtype, y_rows, _ptr(rows),
                                            _ptr(weights), tokens, topk, hidden, _ptr(dy), _ptr(dweights),
                                            _stream(stream)), "fpq_moe_combine_backward")
+
+
+def fpq_moe_combine_backward_full(dout, dout_dtype, y, y_dtype, y_rows, rows, weights, tokens, topk, hidden, dy,
+                                  dweights, workspace=None, stream=None):
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().fpq_moe_combine_backward_full(_ptr(dout), dout_dtype, _ptr(y), y_dtype, y_rows, _ptr(rows),
+                                                _ptr(weights), tokens, topk, hidden, _ptr(dy), _ptr(dweights),
+                                                _ptr(workspace), wsb, _stream(stream)),
+           "fpq_moe_combine_backward_full")
 
 
 def fpq_gemv_nvfp4(x, m, wq, ws, wg, n, k, y, y_dtype, stream=None):

@@ -719,6 +719,17 @@ fpq_status check_combine(int64_t y_rows, const int32_t* rows, int64_t tokens, in
     }
     return FPQ_OK;
 }
+
+fpq_status check_combine_backward(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype, int64_t y_rows,
+                                  const int32_t* rows, const float* weights, int64_t tokens, int32_t topk,
+                                  int64_t hidden, const void* dy, const float* dweights) {
+    fpq_status st = check_combine(y_rows, rows, tokens, topk, hidden, y_dtype, dout_dtype);
+    if (st != FPQ_OK || tokens == 0) return st;
+    if ((st = check_ptrs({dout, weights, dweights})) != FPQ_OK) return st;
+    if (y_rows > 0 && (st = check_ptrs({y, dy})) != FPQ_OK) return st;
+    if (rows && !aligned16(rows)) { set_detail("pointer not 16-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    return FPQ_OK;
+}
 }  // namespace
 
 fpq_status fpq_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, const int32_t* rows, const float* weights,
@@ -745,18 +756,46 @@ fpq_status fpq_moe_combine_backward(const void* dout, int32_t dout_dtype, const 
                                     int64_t y_rows, const int32_t* rows, const float* weights, int64_t tokens,
                                     int32_t topk, int64_t hidden, void* dy, float* dweights, void* stream) {
     t_detail[0] = 0;
-    fpq_status st = check_combine(y_rows, rows, tokens, topk, hidden, y_dtype, dout_dtype);
-    if (st != FPQ_OK) return st;
-    if (tokens == 0) return FPQ_OK;
-    if ((st = check_ptrs({dout, weights, dweights})) != FPQ_OK) return st;
-    if (y_rows > 0 && (st = check_ptrs({y, dy})) != FPQ_OK) return st;
-    if (rows && !aligned16(rows)) { set_detail("pointer not 16-byte aligned"); return FPQ_ERR_ALIGNMENT; }
+    fpq_status st = check_combine_backward(dout, dout_dtype, y, y_dtype, y_rows, rows, weights, tokens, topk, hidden,
+                                           dy, dweights);
+    if (st != FPQ_OK || tokens == 0) return st;
     const DeviceState* d = device_state(&st);
     if (!d) return st;
     return from_cuda(fpq::launch_moe_combine_backward(dout, dout_dtype == FPQ_OUT_F32, y, y_dtype == FPQ_OUT_F32,
                                                       y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
-                                                      d->err, d->sms, (cudaStream_t)stream),
+                                                      nullptr, d->err, d->sms, (cudaStream_t)stream),
                      "moe combine backward launch");
+}
+
+fpq_status fpq_moe_combine_backward_full(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype,
+                                         int64_t y_rows, const int32_t* rows, const float* weights, int64_t tokens,
+                                         int32_t topk, int64_t hidden, void* dy, float* dweights, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    t_detail[0] = 0;
+    fpq_status st = check_combine_backward(dout, dout_dtype, y, y_dtype, y_rows, rows, weights, tokens, topk, hidden,
+                                           dy, dweights);
+    if (st != FPQ_OK || (tokens == 0 && y_rows == 0)) return st;
+    const int64_t pairs = tokens * topk;
+    const int32_t* const map = pairs ? rows : nullptr;      // of no tokens there is none, and no row is named
+    if (map && y_rows > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)y_rows * 4)) {
+        set_detail("need a 16-byte aligned workspace of 4 bytes per row of y");
+        return FPQ_ERR_WORKSPACE;
+    }
+    if (y_rows > 0 && (st = check_ptrs({dy})) != FPQ_OK) return st;
+    const DeviceState* d = device_state(&st);
+    if (!d) return st;
+    int32_t* const owner = map && y_rows > 0 ? (int32_t*)workspace : nullptr;
+    if (pairs) {
+        st = from_cuda(fpq::launch_moe_combine_backward(dout, dout_dtype == FPQ_OUT_F32, y, y_dtype == FPQ_OUT_F32,
+                                                        y_rows, rows, weights, tokens, topk, hidden, dy, dweights,
+                                                        owner, d->err, d->sms, (cudaStream_t)stream),
+                       "moe combine backward launch");
+        if (st != FPQ_OK) return st;
+    }
+    if (y_rows == 0 || (!map && y_rows == pairs)) return FPQ_OK;       // every row is named
+    return from_cuda(fpq::launch_moe_clear_rows(map, pairs, y_rows, owner, hidden * (y_dtype == FPQ_OUT_F32 ? 4 : 2),
+                                                dy, (cudaStream_t)stream),
+                     "moe combine backward rows launch");
 }
 
 namespace {

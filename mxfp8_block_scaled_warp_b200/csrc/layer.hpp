@@ -40,8 +40,12 @@ cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const i
                                uint32_t* err, cudaStream_t st);
 cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
                                         const int32_t* rows, const float* weights, int64_t tokens, int topk,
-                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, int sms,
-                                        cudaStream_t st);
+                                        int64_t hidden, void* dy, float* dweights, int32_t* owner, uint32_t* err,
+                                        int sms, cudaStream_t st);
+// Zeros into the rows of dy that no pair names; owner as written by the
+// backward call (unused without rows).
+cudaError_t launch_moe_clear_rows(const int32_t* rows, int64_t pairs, int64_t y_rows, const int32_t* owner,
+                                  int64_t row_bytes, void* dy, cudaStream_t st);
 
 // Few rows times NVFP4 weights (gemv_nvfp4.cu): row m of y [m, n] is row
 // m / x_div of x times the matrix (ids == nullptr) or expert ids[m]'s.

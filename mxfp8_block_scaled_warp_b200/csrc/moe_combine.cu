@@ -75,6 +75,7 @@ struct CombineArgs {
     void* out;                  // forward: [tokens, hidden]; backward: dy
     float* dweights;
     uint32_t* err;
+    int32_t* owner;             // backward: [y_rows], or nullptr; a named row's gets its pair
 };
 
 // Row of pair p, -1 if it is dropped or outside the buffer.
@@ -169,6 +170,7 @@ moe_combine_bwd_kernel(const CombineArgs a) {
         for (int j = 0; j < KB; ++j) {
             const int64_t p = tok * a.topk + j0 + j;
             r[j] = j0 + j < a.topk ? pair_row(a, p, t == 0) : -1;
+            if (a.owner && t == 0 && r[j] >= 0) a.owner[r[j]] = (int32_t)p;
             w[j] = r[j] >= 0 ? __ldg(a.weights + p) : 0.0f;
             dot[j] = 0.0f;
         }
@@ -224,6 +226,30 @@ moe_combine_bwd_kernel(const CombineArgs a) {
             }
             __syncthreads();
         }
+    }
+}
+
+// Zeros into the rows of dy that no pair names.  A row is named if its owner is
+// a pair that names it, so the owners need no initial value: what an unnamed
+// row's memory holds is no pair, or one with another row.  A row per thread,
+// the unnamed ones written by the whole warp; with none a launch, 2 us.
+constexpr int kClearThreads = 256;
+
+__global__ void __launch_bounds__(kClearThreads)
+moe_clear_rows_kernel(const int32_t* rows, int64_t pairs, int64_t y_rows, const int32_t* owner, int64_t row_vecs,
+                      uint4* dy) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * kClearThreads + threadIdx.x, first = r - lane;
+    bool unnamed = false;
+    if (r < y_rows) {
+        const int64_t p = rows ? owner[r] : r;
+        unnamed = p < 0 || p >= pairs || (rows && rows[p] != r);
+    }
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, unnamed); left; left &= left - 1) {
+        uint4* const row = dy + (first + __ffs(left) - 1) * row_vecs;
+        for (int64_t v = lane; v < row_vecs; v += 32) st_v4(row + v, make_uint4(0, 0, 0, 0));
     }
 }
 
@@ -315,7 +341,8 @@ cudaError_t by_types(bool y32, bool o32, int topk, F&& f) {
 cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const int32_t* rows, const float* weights,
                                int64_t tokens, int topk, int64_t hidden, const void* add, void* out, int out_f32,
                                uint32_t* err, cudaStream_t st) {
-    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), add, nullptr, out, nullptr, err};
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), add, nullptr, out, nullptr, err,
+                        nullptr};
     return by_types(y_f32 != 0, out_f32 != 0, topk, [&](auto y32, auto o32, auto kb) {
         return combine<decltype(y32)::value, decltype(o32)::value, decltype(kb)::value>(a, st);
     });
@@ -323,12 +350,19 @@ cudaError_t launch_moe_combine(const void* y, int y_f32, int64_t y_rows, const i
 
 cudaError_t launch_moe_combine_backward(const void* dout, int dout_f32, const void* y, int y_f32, int64_t y_rows,
                                         const int32_t* rows, const float* weights, int64_t tokens, int topk,
-                                        int64_t hidden, void* dy, float* dweights, uint32_t* err, int sms,
-                                        cudaStream_t st) {
-    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), nullptr, dout, dy, dweights, err};
+                                        int64_t hidden, void* dy, float* dweights, int32_t* owner, uint32_t* err,
+                                        int sms, cudaStream_t st) {
+    const CombineArgs a{y, y_rows, rows, weights, tokens, topk, (int)(hidden / 8), nullptr, dout, dy, dweights, err,
+                        owner};
     return by_types(y_f32 != 0, dout_f32 != 0, topk, [&](auto y32, auto d32, auto kb) {
         return combine_backward<decltype(y32)::value, decltype(d32)::value, decltype(kb)::value>(a, sms, st);
     });
+}
+
+cudaError_t launch_moe_clear_rows(const int32_t* rows, int64_t pairs, int64_t y_rows, const int32_t* owner,
+                                  int64_t row_bytes, void* dy, cudaStream_t st) {
+    return launch_pdl(moe_clear_rows_kernel, dim3((unsigned)((y_rows + kClearThreads - 1) / kClearThreads)),
+                      dim3(kClearThreads), 0, st, rows, pairs, y_rows, owner, row_bytes / 16, (uint4*)dy);
 }
 
 }  // namespace fpq

@@ -216,11 +216,21 @@ py::tuple moe_combine_backward(const Tensor& dout, const Tensor& y, const Tensor
     need(!dy_buffer || is(*dy_buffer, y.scalar_type(), y.sizes()), "need dy of y's type and shape");
     const int32_t type = out_type(y.scalar_type()), d_type = out_type(dout.scalar_type());
     Call call(y, {&dout, &weights, ptr(rows), ptr(dy_buffer)});
-    Tensor dy = dy_buffer ? *dy_buffer : at::empty(y.sizes(), y.options());
     Tensor dweights = empty(y, weights.sizes(), at::kFloat);
-    check(fpq_moe_combine_backward(dout.data_ptr(), d_type, y.data_ptr(), type, y_rows, as<int32_t>(rows),
-                                   as<float>(weights), tokens, (int32_t)weights.size(1), hidden, dy.data_ptr(),
-                                   as<float>(dweights), call.stream), "fpq_moe_combine_backward");
+    if (dy_buffer) {
+        check(fpq_moe_combine_backward(dout.data_ptr(), d_type, y.data_ptr(), type, y_rows, as<int32_t>(rows),
+                                       as<float>(weights), tokens, (int32_t)weights.size(1), hidden,
+                                       dy_buffer->data_ptr(), as<float>(dweights), call.stream),
+              "fpq_moe_combine_backward");
+        return py::make_tuple(*dy_buffer, dweights);
+    }
+    Tensor dy = empty(y, y.sizes(), y.scalar_type());
+    const int64_t bytes = rows ? 4 * y_rows : 0;
+    Tensor ws = empty(y, {bytes}, at::kByte);
+    check(fpq_moe_combine_backward_full(dout.data_ptr(), d_type, y.data_ptr(), type, y_rows, as<int32_t>(rows),
+                                        as<float>(weights), tokens, (int32_t)weights.size(1), hidden, dy.data_ptr(),
+                                        as<float>(dweights), ws.data_ptr(), (size_t)bytes, call.stream),
+          "fpq_moe_combine_backward_full");
     return py::make_tuple(dy, dweights);
 }
 

@@ -219,10 +219,9 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor,
                      dy: torch.Tensor | None = None, stream=None):
     """Gradients of combine for the gradient dout (bf16 or fp32 [tokens,
     hidden]) of its result: (dy of y's type and shape, dweights fp32 [tokens,
-    topk]); add's gradient is dout itself.  Rows of dy that no pair names are
-    left as they were in the buffer: pass a zeroed `dy` where there are such
-    rows, a new buffer is not initialised.  A row may be named by one pair
-    only."""
+    topk]); add's gradient is dout itself.  Rows that no pair names are zero in
+    a new dy, and left as they were in the buffer `dy` if one is given (not y's
+    or dout's memory).  A row may be named by one pair only."""
     if stream is not None:
         with _on_stream(stream, y):
             return combine_backward(dout, y, weights, rows, dy)

@@ -193,3 +193,13 @@ def test_gate_backward_refuses_a_gradient_over_its_logits(lib):
             assert call(P + shift, P, dtype) == INVALID and b"overlap" in lib.fpq_last_error_detail()
     if not torch.cuda.is_available():                        # beside each other: as far as the device
         assert call(P, P + size) == UNSUPPORTED and call(P + size, P) == UNSUPPORTED
+
+
+def test_combine_backward_of_every_row(lib):
+    # dout dtype y dtype y_rows rows weights tokens topk hidden dy dweights ws wsb stream
+    good = [P, 1, P, 0, 128, P, P, 16, 8, 64, P, P, P, 512, None]
+    _refused(lib.fpq_moe_combine_backward_full, good, [
+        ({1: 5}, INVALID), ({9: 4}, INVALID), ({5: None, 4: 100}, INVALID), ({0: None}, INVALID), ({10: None}, INVALID),
+        ({11: None}, INVALID), ({5: P + 4}, ALIGNMENT), ({10: P + 8}, ALIGNMENT), ({12: None}, WORKSPACE),
+        ({12: P + 4}, WORKSPACE), ({13: 511}, WORKSPACE), ({7: 0, 10: None}, INVALID)])
+    assert lib.fpq_moe_combine_backward_full(*(good[:4] + [0] + good[5:7] + [0] + good[8:])) == 0     # nothing to write

@@ -169,3 +169,59 @@ def test_many_tokens_without_a_row_map(fpq):
     assert torch.equal(dw[keep], full_dw[keep]) and torch.all(dw[~keep] == 0)
     assert torch.equal(dy.view(2600, 8, 64)[keep], full_dy.view(2600, 8, 64)[keep])
     assert torch.all(dy.view(2600, 8, 64)[~keep] == 0)
+
+
+@pytest.mark.parametrize("tokens,topk,hidden", [(4, 3, 264), (2600, 2, 72), (300, 8, 2048)])
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+def test_rows_that_no_pair_names_have_no_gradient(fpq, tokens, topk, hidden, y_dtype):
+    """A new buffer holds zeros there, whatever its memory held before."""
+    y, rows, w, _ = _case(tokens, topk, hidden, 17, y_dtype, extra=70)
+    rows[1, 0] = -1
+    rows[tokens - 1] = -1
+    named = torch.zeros(y.shape[0], dtype=torch.bool, device="cuda")
+    named[rows[rows >= 0].long()] = True
+    dout = torch.randn((tokens, hidden), device="cuda").to(torch.bfloat16)
+    want, want_w = moe.combine_backward(dout, y, w, rows=rows, dy=torch.zeros_like(y))
+    for _ in range(3):
+        used = [torch.full_like(y, float("nan")) for _ in range(3)]
+        used += [torch.zeros((y.shape[0],), dtype=torch.int32, device="cuda")]
+        del used
+        dy, dw = moe.combine_backward(dout, y, w, rows=rows)
+        assert torch.equal(dy, want) and torch.equal(dw, want_w)
+    assert torch.all(dy[~named] == 0)
+    # without a map the first tokens * topk rows are named
+    used = [torch.full_like(y, float("nan")) for _ in range(3)]
+    del used
+    dy, _ = moe.combine_backward(dout, y, w)
+    assert torch.all(torch.isfinite(dy)) and torch.all(dy[tokens * topk:] == 0)
+    assert torch.all(moe.combine_backward(dout, y, w, rows=torch.full_like(rows, -1))[0] == 0)
+    assert fpq.fpq_get_device_error() == 0
+
+
+def test_no_tokens_but_rows(fpq):
+    y = torch.ones((40, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.empty((0, 4), device="cuda")
+    used = [torch.full_like(y, float("nan")) for _ in range(3)]
+    del used
+    for rows in (None, torch.empty((0, 4), dtype=torch.int32, device="cuda")):
+        dy, dw = moe.combine_backward(y[:0], y, w, rows=rows)
+        assert torch.all(dy == 0) and dw.shape == (0, 4)
+
+
+def test_every_row_written_from_any_workspace(fpq):
+    """The C entry with a workspace that held the owners of another map, whose
+    pairs name other rows now."""
+    y, rows, w, _ = _case(50, 4, 64, 19, torch.bfloat16, extra=30)
+    dout = torch.randn((50, 64), device="cuda").to(torch.bfloat16)
+    ws = torch.empty((y.shape[0] + 4,), dtype=torch.int32, device="cuda")
+    ws[-4:] = 9
+    dw = torch.empty_like(w)
+    for turn in range(3):
+        rows = (rows + 17) % y.shape[0]                          # each row still named once
+        named, rows = rows, rows.clone()
+        rows[turn, 1] = -1
+        dy = torch.full_like(y, float("nan"))
+        fpq.fpq_moe_combine_backward_full(dout, 0, y, 0, y.shape[0], rows, w, 50, 4, 64, dy, dw, ws)
+        want, want_w = moe.combine_backward(dout, y, w, rows=rows, dy=torch.zeros_like(y))
+        assert torch.equal(dy, want) and torch.equal(dw, want_w) and torch.all(ws[-4:] == 9)
+        rows = named
