@@ -520,6 +520,10 @@ FPQ_API fpq_status fpq_grouped_scaled_gemm(fpq_format fmt, const void* aq, const
  * bf16, by the rule of fpq_quantize_block (FP8_1x128: the rounding of the
  * correctly rounded fp32 quotient of y and the scale, which is 1 where amax /
  * 448 rounds to 0).  Other overlaps between inputs and outputs are not allowed.
+ * rstd and y come from the fp32 sum s, not from h, its rounding.  The order in
+ * which a row's squares are added depends on cols and, past 1024 columns, on
+ * whether the call has fewer than two rows per SM: the same row in a small and
+ * in a large call may differ in its last places.
  *
  * Requires 0 <= rows < 2^31, cols a multiple of 8 in [8, 32768] (of 128 with
  * FPQ_FP8_1x128 codes, of 32 with FPQ_MXFP8), ld_x >= cols a multiple of 8,
@@ -541,7 +545,8 @@ FPQ_API fpq_status fpq_rmsnorm_quantize(fpq_format fmt, const void* x, int64_t l
  *
  *   dy         bf16 [rows, cols]
  *   x          the normed rows: x (row stride ld_x elements), or h where a
- *              residual was added
+ *              residual was added (the gradient is then taken at h, the bf16
+ *              rounding of the sum that the forward normed)
  *   rstd       fp32 [rows] as written by the forward
  *   dres       bf16 [rows, cols], or NULL
  *   dx         bf16 [rows, cols] (output; may be dy's or dres's buffer)
@@ -572,7 +577,8 @@ FPQ_API fpq_status fpq_rmsnorm_backward(const void* dy, const void* x, int64_t l
  *            the topk_group best groups are chosen
  *   ids      the topk largest keys in descending order
  *   weights  scale score_e; with renormalize divided by the sum of the
- *            chosen experts' scores (0 where that sum is 0)
+ *            chosen experts' scores (0 where that sum is 0: an fp32 sigmoid is
+ *            0 for logits below -88.7)
  * Keys and ranks are compared as in exact arithmetic (fp64 where fp32 cannot
  * tell two apart); equal ones go to the lowest index.  The bias enters the
  * choice alone.

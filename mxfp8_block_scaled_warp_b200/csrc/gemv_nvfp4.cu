@@ -36,9 +36,13 @@
 // TB/s), 8 rows 35.5, 16 rows 45; 2048 x 7168, one row 5.2; 8 tokens x 8 of
 // 64 experts, 2048 x 7168, 83 us, 32 tokens 159.  Bound by the data pipe of
 // the L1 (70% busy for 8 tokens, 80 for 16 rows): a load of codes takes a
-// cycle for each of the eight rows that it touches, and x is read from
-// shared memory in the width of the decoded weights for every eight columns.
-// Its conversion is another 8 us of the 45.  Not better, and not here: loads
+// cycle for each of the eight rows that it touches, so does each of a block's
+// two 16-bit loads of scales, an eighth of the bytes, and x is read from
+// shared memory in the width of the decoded weights for every eight columns,
+// those past the last too.  Its conversion is another 8 us of the 45; the
+// sixteen-column kernels spill 40 bytes at 128 registers.  One token through
+// one expert takes 11.6 us, where the launch rule's eight experts leave most
+// SMs without a CTA.  Not better, and not here: loads
 // of 32 bytes, half as many for the pipe (8 tokens 82 us, but 16 rows 48 and
 // one 31: fewer, larger pieces on their way); 24 or 32 warps of fewer
 // registers (16 rows 49 and 59, 8 tokens 88 and 92); the blocks through a

@@ -16,8 +16,9 @@
 // bytes in flight: one vector of eight rows, two of four or four of two
 // (with one vector of two rows 16000 tokens x 2048, two choices took 61 us
 // forward and 152 back; with four of two 39 and 53).  Measured, bf16: 8192
-// tokens x 7168, eight choices and an addend 185 us (6.34 TB/s), back 329 us
-// (6.07 TB/s); 16 tokens 2.6 and 5.7 us, which is latency.
+// tokens x 7168, eight choices and an addend 185 us (6.34 TB/s), back 338 us
+// (5.91 TB/s); 16 tokens 2.6 and 5.7 us, which is latency.  Zeros in the rows
+// that no pair names, where they are asked for, take 2 to 4 us more.
 #include <type_traits>
 
 #include <cuda_runtime.h>
