@@ -225,3 +225,22 @@ def test_every_row_written_from_any_workspace(fpq):
         want, want_w = moe.combine_backward(dout, y, w, rows=rows, dy=torch.zeros_like(y))
         assert torch.equal(dy, want) and torch.equal(dw, want_w) and torch.all(ws[-4:] == 9)
         rows = named
+
+
+def test_backward_with_a_row_map_captured(fpq):
+    """Replayed with other maps and dropped pairs; the gradient and its zeros follow."""
+    y, rows, w, _ = _case(120, 4, 264, 23, torch.bfloat16, extra=60)
+    dout = torch.randn((120, 264), device="cuda").to(torch.bfloat16)
+    moe.combine_backward(dout, y, w, rows=rows)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dy, dw = moe.combine_backward(dout, y, w, rows=rows)
+    for turn in range(4):
+        other = torch.randperm(y.shape[0], generator=torch.Generator().manual_seed(turn))[:480].view(120, 4).int().cuda()
+        other[turn::7, turn] = -1
+        rows.copy_(other)
+        dy.fill_(float("nan"))
+        g.replay()
+        want, want_w = moe.combine_backward(dout, y, w, rows=rows, dy=torch.zeros_like(y))
+        assert torch.equal(dy, want) and torch.equal(dw, want_w)
