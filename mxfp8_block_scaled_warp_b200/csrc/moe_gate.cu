@@ -223,12 +223,12 @@ moe_gate_kernel(const GateArgs a) {
         const float rank = a.group_top == 2 ? first + second : first;
         const bool holds = g < a.n_group && (lane & (split - 1)) == 0;
         uint32_t gkey = holds ? pattern(rank) : kTaken;
-        // each group counts the ranks above its own; only where two are too
-        // near to tell are the best taken one after the other
         // twice the rank's error: each key has its own, by its own magnitude,
         // which the sum may fall far below; the addition's step is within them
         const float own = value(gkey);
         const float reach = fabsf(own) < INFINITY ? slack(first) + (a.group_top == 2 ? slack(second) : 0.0f) : 0.0f;
+        // each group counts the ranks above its own; only where two are too
+        // near to tell are the best taken one after the other
         int above = 0;
         bool close = false;
 #pragma unroll 4
